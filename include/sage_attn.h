@@ -341,6 +341,57 @@ int sage_attn_fwd_host_variant(const void* q, const void* k, const void* v, void
                                int causal, float sm_scale, int granularity, int heads_per_chunk, int variant,
                                void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Serving operators around the attention forward pass (not operations of the pages: what a model
+ * needs next to it).  Conventions of this section:
+ *   - dtype is SAGE_F16 or SAGE_BF16, the element type of every activation, weight and cache
+ *     (cos, sin: fp32); d is 64 or 128; sums, norms and softmax statistics are fp32 and each
+ *     output is rounded once.
+ *   - Activations are strided views: sage_strides holds the element strides of batch, head and
+ *     token (host memory, read during the call), the channel stride is 1.  A paged cache is the
+ *     view [page][head][token in page][d] (b = page stride).  Every base pointer is 16-byte
+ *     aligned; every stride of a dimension larger than 1 is positive and a multiple of 8 elements.
+ *   - page_size is 16, 32, 64, 128 or 256 tokens; num_pages * page_size stays below 2^31.
+ *   - Index arrays (positions, slots, page_table, cu_q, kv_len, key_len) are int32 device memory,
+ *     dense.  Their values are not known to the host: the kernels check them as stated and never
+ *     access memory outside the tensors.
+ *   - A call with no token to work on (B, T or N = 0) returns SAGE_OK and launches nothing.
+ * Statuses, streams and ordering as above.  Every call can be captured into a CUDA graph. */
+enum { SAGE_F16 = 0, SAGE_BF16 = 1 };
+typedef struct {
+  int64_t b, h, n; /* elements from one batch entry (or page), head, token to the next */
+} sage_strides;
+
+/* Norm of each query and key head and the position rotation, in one pass.  For every token and
+ * head, with x its d channels: y = x * rsqrt(mean(x^2) + eps) * weight (weight NULL: y = x); the
+ * pairs (i, i + rot_dim/2) of y's first rot_dim channels -- (2i, 2i+1) when interleaved -- become
+ * (a cos_i - b sin_i, b cos_i + a sin_i) with row `position` of cos and sin; channels past rot_dim
+ * stay y.  rot_dim is a multiple of 16, 16 .. d.
+ * q: [B,Hq,N,d], k: [B,Hk,N,d] (in; k may be NULL with Hk = 0); q_out, k_out the same shapes (out;
+ * either may be its input itself, with the same strides, else no overlap); q_weight, k_weight: [d]
+ * or NULL; cos, sin: fp32 [table_rows, rot_dim/2] dense, 16-byte aligned; positions: [N] when
+ * positions_per_batch is 0, [B,N] when it is 1, or NULL (token n has position n; table_rows >= N).
+ * A token whose position is outside the tables gets NaN in all its rows.  eps >= 0, finite. */
+int sage_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const sage_strides* q_st,
+                      const sage_strides* k_st, const sage_strides* q_out_st, const sage_strides* k_out_st,
+                      const void* q_weight, const void* k_weight, const float* cos, const float* sin,
+                      const int32_t* positions, int positions_per_batch, int B, int Hq, int Hk, int N, int d,
+                      int rot_dim, int table_rows, int interleaved, float eps, int dtype, void* stream);
+
+/* The same for the T new tokens of a serving step (b strides of q, k, v, q_out unused), with the
+ * key heads and v written into the paged cache: token t's K and V go to page slots[t] / page_size,
+ * row slots[t] % page_size; a slot outside [0, num_pages * page_size) (padding: -1) writes neither.
+ * Tokens must not share a slot: one that two tokens name ends up holding parts of either.
+ * q: [T,Hq,d], k, v: [T,Hk,d] (in), q_out: [T,Hq,d] (out; may be q itself), k_cache, v_cache:
+ * [num_pages][Hk][page_size][d] (in place), positions: [T] or NULL, slots: [T]. */
+int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                             const sage_strides* q_st, const sage_strides* k_st, const sage_strides* v_st,
+                             const sage_strides* q_out_st, const sage_strides* k_cache_st,
+                             const sage_strides* v_cache_st, const void* q_weight, const void* k_weight,
+                             const float* cos, const float* sin, const int32_t* positions, const int32_t* slots,
+                             int T, int Hq, int Hk, int d, int rot_dim, int table_rows, int num_pages, int page_size,
+                             int interleaved, float eps, int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

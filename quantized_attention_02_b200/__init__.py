@@ -32,8 +32,15 @@ SAGE_ERR_NOMEM = -5
 SAGE_ERR_TOO_LARGE = -6
 SAGE_PER_TOKEN = 0
 SAGE_PER_BLOCK = 1
+SAGE_F16 = 0
+SAGE_BF16 = 1
 
 _lib = None
+
+
+class SageStrides(ctypes.Structure):
+    """sage_strides of include/sage_attn.h: element strides of batch (or page), head and token."""
+    _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
 
 
 def get_lib() -> ctypes.CDLL:
@@ -75,7 +82,10 @@ def get_lib() -> ctypes.CDLL:
         lib.sage_debug_wait_timeout.argtypes = [_p, _p]
         lib.sage_attn_fwd_host.argtypes = [_p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _i, _i, _p]
         lib.sage_attn_fwd_host_variant.argtypes = [_p, _p, _p, _p, _i, _i, _i, _i, _i, _f, _i, _i, _i, _p]
-        for n in ("sage_smooth_k", "sage_quant_qk", "sage_attn_fwd", "sage_attn_fwd_quantized",
+        _st = ctypes.POINTER(SageStrides)
+        lib.sage_qk_norm_rope.argtypes = [_p] * 4 + [_st] * 4 + [_p] * 5 + [_i] * 9 + [_f, _i, _p]
+        lib.sage_qk_norm_rope_append.argtypes = [_p] * 6 + [_st] * 6 + [_p] * 6 + [_i] * 9 + [_f, _i, _p]
+        for n in ("sage_qk_norm_rope", "sage_qk_norm_rope_append", "sage_smooth_k", "sage_quant_qk", "sage_attn_fwd", "sage_attn_fwd_quantized",
                   "sage_debug_qk_int32", "sage_last_device_error", "sage_attn_fwd_noalloc",
                   "sage_debug_attn_trace", "sage_debug_mma_peak", "sage_attn_fwd_host",
                   "sage_debug_wait_timeout", "sage_quant_v_fp8", "sage_attn_fwd_fp8pv_quantized", "sage_prep_qk",
@@ -422,3 +432,162 @@ def sageattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = F
     else:
         sage_attn_fwd(q, k, v, o, causal, sm_scale, granularity, stream)
     return o
+
+
+# ------------------------------------------------------------------ serving operators
+_DTYPE_CODES = {torch.float16: SAGE_F16, torch.bfloat16: SAGE_BF16}
+
+
+def _data(t: torch.Tensor):
+    return t.data_ptr() or None
+
+
+def _same(name: str, t, like: torch.Tensor, dtype, shape=None) -> None:
+    """t is a CUDA tensor on like's device, of this element type and (where given) shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device (there is no CPU path)")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _dense(name: str, t, like: torch.Tensor, dtype, shape=None):
+    """Pointer of a dense array (None stays None)."""
+    if t is None:
+        return None
+    _same(name, t, like, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return _data(t)
+
+
+def _view(name: str, t, like: torch.Tensor, shape, order):
+    """(pointer, strides) of a view with the channels innermost; order: the dimensions that are batch
+    (or page; None: no such dimension), head and token."""
+    _same(name, t, like, like.dtype, shape)
+    st = t.stride()
+    if t.shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must have its last dimension contiguous")
+    return _data(t), SageStrides(*(0 if i is None else st[i] for i in order))
+
+
+def _activations(q, dims: int, what: str):
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("expected a torch tensor")
+    if not q.is_cuda:
+        raise ValueError("tensor must live on a CUDA device (there is no CPU path)")
+    if q.dim() != dims:
+        raise ValueError(f"expected {what}")
+    if q.dtype not in _DTYPE_CODES:
+        raise ValueError(f"expected float16 or bfloat16, not {q.dtype}")
+    return _DTYPE_CODES[q.dtype]
+
+
+def _call(fn, where: str, device: torch.device, stream, *args) -> None:
+    """fn(*args, stream) with `device` current; stream None: the device's current stream."""
+    handle = torch.cuda.current_stream(device).cuda_stream if stream is None else (
+        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, handle)
+    _check(rc, where)
+
+
+def _empty(shape, like: torch.Tensor, stream) -> torch.Tensor:
+    """A dense output for a launch on `stream`, allocated on that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _tables(cos, sin, q):
+    if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+        raise ValueError("cos and sin must be [table_rows, rot_dim / 2] tensors")
+    return _dense("cos", cos, q, torch.float32), _dense("sin", sin, q, torch.float32, cos.shape)
+
+
+def sage_qk_norm_rope(q, k, q_out, k_out, cos, sin, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      interleaved: bool = False, stream=None) -> None:
+    """Norm of each head of q [B, Hq, N, d] and k [B, Hk, N, d] (k and k_out may be None) and the position
+    rotation, into q_out and k_out: strided fp16 or bf16 views with contiguous channels.  positions: int32
+    [N] or [B, N], rows of cos / sin [table_rows, rot_dim / 2] (fp32); None: token n has position n."""
+    dtype = _activations(q, 4, "a [B, H, N, d] tensor")
+    B, Hq, N, d = q.shape
+    qp, qs = _view("q", q, q, None, (0, 1, 2))
+    qop, qos = _view("q_out", q_out, q, q.shape, (0, 1, 2))
+    kp = kop = ks = kos = None
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        kp, ks = _view("k", k, q, (B, Hk, N, d), (0, 1, 2))
+        kop, kos = _view("k_out", k_out, q, (B, Hk, N, d), (0, 1, 2))
+    cp, sp = _tables(cos, sin, q)
+    per_batch = positions is not None and positions.dim() == 2
+    pp = _dense("positions", positions, q, torch.int32, (B, N) if per_batch else (N,))
+    _call(get_lib().sage_qk_norm_rope, "sage_qk_norm_rope", q.device, stream, qp, kp, qop, kop, qs, ks, qos, kos,
+          _dense("q_weight", q_weight, q, q.dtype, (d,)), _dense("k_weight", k_weight, q, q.dtype, (d,)), cp, sp, pp,
+          int(per_batch), B, Hq, Hk, N, d, 2 * cos.shape[1], cos.shape[0], int(bool(interleaved)), float(eps), dtype)
+
+
+def qk_norm_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = False, stream=None):
+    """(q, k) after the norm of each head (weights None: no norm) and the position rotation, as new dense
+    [B, H, N, d] tensors, the layout sageattn takes.  q and k may be any views with contiguous channels,
+    such as the transposed slices of one projection's output; k may be None.  See sage_qk_norm_rope."""
+    _activations(q, 4, "a [B, H, N, d] tensor")
+    q_out = _empty(q.shape, q, stream)
+    k_out = None if k is None else _empty(k.shape, q, stream)
+    sage_qk_norm_rope(q, k, q_out, k_out, cos, sin, positions, q_weight, k_weight, eps, interleaved, stream)
+    return q_out, k_out
+
+
+def _cache(name: str, cache, q, Hk: int, d: int):
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 4:
+        raise ValueError(f"{name} must be a [pages, page_size, Hk, d] tensor")
+    return _view(name, cache, q, (cache.shape[0], cache.shape[1], Hk, d), (0, 2, 1))
+
+
+def sage_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, cos, sin, positions, slots, q_weight=None,
+                             k_weight=None, eps: float = 1e-6, interleaved: bool = False, stream=None) -> None:
+    """sage_qk_norm_rope for the new tokens q [T, Hq, d], k and v [T, Hk, d] of a serving step: the keys and
+    v go to rows `slots` (int32 [T]; slot = page * page_size + row, outside the cache: not written) of
+    k_cache and v_cache [pages, page_size, Hk, d] (strided views; page_size 16 .. 256, a power of two)."""
+    dtype = _activations(q, 3, "a [T, H, d] tensor")
+    T, Hq, d = q.shape
+    Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    order = (None, 1, 0)
+    qp, qs = _view("q", q, q, None, order)
+    kp, ks = _view("k", k, q, (T, Hk, d), order)
+    vp, vs = _view("v", v, q, (T, Hk, d), order)
+    qop, qos = _view("q_out", q_out, q, q.shape, order)
+    kcp, kcs = _cache("k_cache", k_cache, q, Hk, d)
+    vcp, vcs = _cache("v_cache", v_cache, q, Hk, d)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    cp, sp = _tables(cos, sin, q)
+    _call(get_lib().sage_qk_norm_rope_append, "sage_qk_norm_rope_append", q.device, stream, qp, kp, vp, qop, kcp, vcp,
+          qs, ks, vs, qos, kcs, vcs, _dense("q_weight", q_weight, q, q.dtype, (d,)),
+          _dense("k_weight", k_weight, q, q.dtype, (d,)), cp, sp, _dense("positions", positions, q, torch.int32, (T,)),
+          _dense("slots", slots, q, torch.int32, (T,)), T, Hq, Hk, d, 2 * cos.shape[1], cos.shape[0],
+          k_cache.shape[0], k_cache.shape[1], int(bool(interleaved)), float(eps), dtype)
+
+
+def qk_norm_rope_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
+                        eps: float = 1e-6, interleaved: bool = False, stream=None) -> torch.Tensor:
+    """q [T, Hq, d] after the norm and rotation as a new dense tensor; the new tokens' keys (normed and
+    rotated) and values go into the paged cache in the same pass.  See sage_qk_norm_rope_append."""
+    _activations(q, 3, "a [T, H, d] tensor")
+    q_out = _empty(q.shape, q, stream)
+    sage_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, cos, sin, positions, slots, q_weight, k_weight, eps,
+                             interleaved, stream)
+    return q_out
