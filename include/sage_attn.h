@@ -392,6 +392,35 @@ int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* 
                              int T, int Hq, int Hk, int d, int rot_dim, int table_rows, int num_pages, int page_size,
                              int interleaved, float eps, int dtype, void* stream);
 
+/* Attention of new tokens over a paged cache.  Sequence b has nq_b = cu_q[b+1] - cu_q[b] new tokens,
+ * rows cu_q[b] .. of q and o, whose keys and values are in the cache already (the last nq_b of its
+ * kv_len[b] keys when causal); key j stands in page page_table[b][j / page_size], row j % page_size.
+ * o_i = sum_j softmax_j(q_i . k_j * sm_scale) v_j over the keys the token sees: all kv_len[b] of them,
+ * or, causal, keys j <= kv_len[b] - nq_b + i; query head h uses key head h / (Hq/Hk).  A token that
+ * sees no key (kv_len < nq, or 0) gets 0.  Rows of o outside [cu_q[0], cu_q[B]) stay as they were.
+ * Single tokens (nq_b = 1) and chunks of different lengths may be mixed in one call.
+ * q, o: [T,Hq,d] (o may not overlap q), b strides unused; k_cache, v_cache: [num_pages][Hk][page_size][d];
+ * page_table: [B][pages_per_seq]; cu_q: [B+1], ascending; kv_len: [B].  Hq is a multiple of Hk, at most
+ * 128 times it.  Values of kv_len are taken into [0, pages_per_seq * page_size], of cu_q into [0, T];
+ * a page outside the cache reads as zeros.  Cache rows past a sequence's end are never used, whatever
+ * they hold.  When few tokens meet long caches the key axis is split over CTAs and joined (fp32
+ * parts in a stream-ordered workspace), in a fixed order: the same call gives the same bits. */
+int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, void* o, const sage_strides* q_st,
+                    const sage_strides* k_cache_st, const sage_strides* v_cache_st, const sage_strides* o_st,
+                    const int32_t* page_table, const int32_t* cu_q, const int32_t* kv_len, int B, int T, int Hq,
+                    int Hk, int d, int num_pages, int page_size, int pages_per_seq, int causal, float sm_scale,
+                    int dtype, void* stream);
+
+/* Cross attention to states of another length: o_i = sum_j softmax_j(q_i . k_j * sm_scale) v_j over the
+ * keys j < key_len[b] (all Nk when key_len is NULL; values are taken into [0, Nk]).  No key: 0.
+ * q, o: [B,Hq,Nq,d]; k, v: [B,Hk,Nk,d] (may be NULL when Nk = 0); query head h uses key head
+ * h / (Hq/Hk); Hq as above.  Keys past key_len are never used, whatever they hold.  Nq = 1 is a
+ * decoder's single token. */
+int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const sage_strides* q_st,
+                    const sage_strides* k_st, const sage_strides* v_st, const sage_strides* o_st,
+                    const int32_t* key_len, int B, int Hq, int Hk, int Nq, int Nk, int d, float sm_scale, int dtype,
+                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -85,7 +85,9 @@ def get_lib() -> ctypes.CDLL:
         _st = ctypes.POINTER(SageStrides)
         lib.sage_qk_norm_rope.argtypes = [_p] * 4 + [_st] * 4 + [_p] * 5 + [_i] * 9 + [_f, _i, _p]
         lib.sage_qk_norm_rope_append.argtypes = [_p] * 6 + [_st] * 6 + [_p] * 6 + [_i] * 9 + [_f, _i, _p]
-        for n in ("sage_qk_norm_rope", "sage_qk_norm_rope_append", "sage_smooth_k", "sage_quant_qk", "sage_attn_fwd", "sage_attn_fwd_quantized",
+        lib.sage_paged_attn.argtypes = [_p] * 4 + [_st] * 4 + [_p] * 3 + [_i] * 9 + [_f, _i, _p]
+        lib.sage_cross_attn.argtypes = [_p] * 4 + [_st] * 4 + [_p] + [_i] * 6 + [_f, _i, _p]
+        for n in ("sage_paged_attn", "sage_cross_attn", "sage_qk_norm_rope", "sage_qk_norm_rope_append", "sage_smooth_k", "sage_quant_qk", "sage_attn_fwd", "sage_attn_fwd_quantized",
                   "sage_debug_qk_int32", "sage_last_device_error", "sage_attn_fwd_noalloc",
                   "sage_debug_attn_trace", "sage_debug_mma_peak", "sage_attn_fwd_host",
                   "sage_debug_wait_timeout", "sage_quant_v_fp8", "sage_attn_fwd_fp8pv_quantized", "sage_prep_qk",
@@ -591,3 +593,63 @@ def qk_norm_rope_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, q
     sage_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, cos, sin, positions, slots, q_weight, k_weight, eps,
                              interleaved, stream)
     return q_out
+
+
+def sage_paged_attn(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal: bool, sm_scale: float,
+                    stream=None) -> None:
+    """Attention of the new tokens q [T, Hq, d] over a paged cache k_cache, v_cache [pages, page_size, Hk, d]
+    into o [T, Hq, d]: sequence b has rows cu_q[b] .. cu_q[b+1] of q and kv_len[b] keys in the pages of
+    page_table[b].  page_table int32 [B, pages_per_seq], cu_q int32 [B + 1], kv_len int32 [B]."""
+    dtype = _activations(q, 3, "a [T, H, d] tensor")
+    T, Hq, d = q.shape
+    Hk = k_cache.shape[2] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
+    qp, qs = _view("q", q, q, None, (None, 1, 0))
+    op, os_ = _view("o", o, q, q.shape, (None, 1, 0))
+    kp, ks = _cache("k_cache", k_cache, q, Hk, d)
+    vp, vs = _cache("v_cache", v_cache, q, Hk, d)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [B, pages_per_seq] tensor")
+    B, width = page_table.shape
+    _call(get_lib().sage_paged_attn, "sage_paged_attn", q.device, stream, qp, kp, vp, op, qs, ks, vs, os_,
+          _dense("page_table", page_table, q, torch.int32), _dense("cu_q", cu_q, q, torch.int32, (B + 1,)),
+          _dense("kv_len", kv_len, q, torch.int32, (B,)), B, T, Hq, Hk, d, k_cache.shape[0], k_cache.shape[1], width,
+          int(bool(causal)), float(sm_scale), dtype)
+
+
+def sageattn_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, causal: bool = True,
+                   sm_scale: float | None = None, stream=None) -> torch.Tensor:
+    """O = softmax(Q K^T sm_scale) V of new tokens over a paged cache, fp16 or bf16, as a new dense
+    [T, Hq, d] tensor (rows outside every sequence are not written); sm_scale defaults to d^-1/2.
+    See sage_paged_attn; the cache is filled by qk_norm_rope_append."""
+    _activations(q, 3, "a [T, H, d] tensor")
+    o = _empty(q.shape, q, stream)
+    sage_paged_attn(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal,
+                    1.0 / math.sqrt(q.shape[-1]) if sm_scale is None else sm_scale, stream)
+    return o
+
+
+def sage_cross_attn(q, k, v, o, key_len, sm_scale: float, stream=None) -> None:
+    """Cross attention of q [B, Hq, Nq, d] to k, v [B, Hk, Nk, d] into o [B, Hq, Nq, d]; key_len int32 [B]
+    (None: all Nk): keys past it are not used.  Strided views with contiguous channels."""
+    dtype = _activations(q, 4, "a [B, H, N, d] tensor")
+    B, Hq, Nq, d = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, Hk, Nk, d] tensor")
+    Hk, Nk = k.shape[1], k.shape[2]
+    qp, qs = _view("q", q, q, None, (0, 1, 2))
+    kp, ks = _view("k", k, q, (B, Hk, Nk, d), (0, 1, 2))
+    vp, vs = _view("v", v, q, (B, Hk, Nk, d), (0, 1, 2))
+    op, os_ = _view("o", o, q, q.shape, (0, 1, 2))
+    _call(get_lib().sage_cross_attn, "sage_cross_attn", q.device, stream, qp, kp, vp, op, qs, ks, vs, os_,
+          _dense("key_len", key_len, q, torch.int32, (B,)), B, Hq, Hk, Nq, Nk, d, float(sm_scale), dtype)
+
+
+def sageattn_cross(q, k, v, key_len=None, sm_scale: float | None = None, stream=None) -> torch.Tensor:
+    """O = softmax(Q K^T sm_scale) V of q [B, Hq, Nq, d] against states of another length k, v [B, Hk, Nk, d],
+    fp16 or bf16, as a new dense tensor; sm_scale defaults to d^-1/2.  See sage_cross_attn."""
+    _activations(q, 4, "a [B, H, N, d] tensor")
+    o = _empty(q.shape, q, stream)
+    sage_cross_attn(q, k, v, o, key_len, 1.0 / math.sqrt(q.shape[-1]) if sm_scale is None else sm_scale, stream)
+    return o

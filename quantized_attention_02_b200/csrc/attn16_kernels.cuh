@@ -1,0 +1,42 @@
+// attn16_kernels.cuh -- launcher of the 16-bit attention kernel (attn16_kernels.cu) behind the paged
+// attention and the cross attention.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace sage {
+
+struct Attn16Args {
+  void* o;
+  long long o_sb, o_sh, o_sn;   // element strides of O
+  const int32_t* cu_q;          // paged: [B+1] first token of each sequence; null: dense, Nq tokens each
+  const int32_t* kv_len;        // keys of each sequence; null (dense): Nk
+  const int32_t* page_table;    // paged: [B][pages_per_seq]; null: dense
+  int pages_per_seq, num_pages, page_shift;
+  int B, Nq, Nk;                // paged: Nq = all tokens, Nk = pages_per_seq * page size
+  int Hk, G;                    // key heads, query heads per key head
+  int tile_tokens;              // tokens of a 128-row query tile: 128 / G
+  int slots;                    // query tile slots of the grid
+  int splits, min_chunk;        // key axis: at most splits parts of at least min_chunk key tiles
+  float* part_o;                // [token][head][splits][D] fp32, unnormalised (splits > 1)
+  float2* part_ml;              // [token][head][splits] (row maximum in log2 units, row sum)
+  float scale_log2;             // sm_scale * log2(e)
+  bool causal;
+};
+
+// The tensor maps (16-bit, 128-byte swizzle, boxes of 64 channels):
+//   q: [B][Hk][tokens][G][D], box {64, G, tile_tokens, 1, 1}
+//   k, v: [B or pages][Hk][rows][D], box {64, min(128, page size), 1, 1}
+struct Attn16Launch {
+  Attn16Args a;
+  CUtensorMap tm_q, tm_k, tm_v;
+  int D;
+  bool bf16;
+  bool pair;  // two query tiles per CTA (else one, its key tiles taken by two streams)
+};
+
+cudaError_t launch_attn16(const Attn16Launch& l, cudaStream_t st);
+int read_and_clear_attn16_error(cudaStream_t st, cudaError_t* err);
+
+}  // namespace sage

@@ -27,6 +27,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "attn_common.cuh"
 #include "attn_kernels.cuh"
 #include "fp4_codes.cuh"
 #include "sm100_ptx.cuh"
@@ -63,28 +64,6 @@ struct AttnLayout {
   static constexpr int THREADS = 384;
 };
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float fast_log2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Magic-number integer -> float: for |S| < 2^22 the bits of S + 0x4B400000 are the float
-// 1.5 * 2^23 + S exactly.
-constexpr uint32_t kMagicBits = 0x4B400000u;
-constexpr float kMagicF = 12582912.0f;
-
 // Scale c with its 3 lowest mantissa bits cleared (21 significant bits): kMagicF * c is then
 // exact in fp32 (relative change of c at most 2^-20).
 __device__ __forceinline__ float trim_scale(float c) { return __uint_as_float(__float_as_uint(c) & ~7u); }
@@ -101,12 +80,6 @@ __device__ __forceinline__ float round_up_to(float x, float q) {
   return fabsf(x) < q * 8388608.0f ? ceilf(x / q) * q : x;
 }
 
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Maximum of 64 signed integers held as bits: four independent chains of one 2-input and
 // seven 3-input maxima (4 * (2 + 7 * 2) = 64 elements, x[0..63] exactly).
 __device__ __forceinline__ int imax64(const uint32_t* x) {
@@ -119,26 +92,6 @@ __device__ __forceinline__ int imax64(const uint32_t* x) {
     for (int k = 0; k < 4; ++k) a[k] = __vimax3_s32(a[k], static_cast<int>(x[i + k]), static_cast<int>(x[i + 4 + k]));
   }
   return max(max(a[0], a[1]), max(a[2], a[3]));
-}
-
-template <uint32_t N>
-__device__ __forceinline__ void reg_alloc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <uint32_t N>
-__device__ __forceinline__ void reg_dealloc() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Bounded wait used on exit paths: ignores the abort flag, records a timeout.
-__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (clock64() - t0 > kWaitLimitCycles) {
-      atomicExch(&g_device_error, kDevTimeoutBarrier);
-      return;
-    }
-  }
 }
 
 __device__ __forceinline__ void group_bar(int id) { asm volatile("barrier.sync %0, 128;" ::"r"(id) : "memory"); }

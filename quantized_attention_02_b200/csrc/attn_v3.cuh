@@ -69,27 +69,6 @@ __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
-// exp2 on the FMA pipe for a pair of arguments (Cody-Waite style range reduction plus a
-// polynomial), to take part of the exp2 work off the MUFU unit:
-//   t -> max(t, -126); n = round_to_nearest(t) via the 1.5 * 2^23 add; f = t - n in [-1/2, 1/2];
-//   2^f ~ c0 + c1 f + c2 f^2 + c3 f^3 with coefficients fitted here to the minimax relative error on
-//   [-1/2, 1/2] (max relative error 7.5e-5, below half an fp16 ulp); 2^n by adding n to the
-//   exponent field (n << 23, taken from the low bits of the magic sum).
-__device__ __forceinline__ float2 exp2_poly2(float2 t) {
-  constexpr float c0 = 0.9999281167984009f, c1 = 0.6932609677314758f, c2 = 0.2426108568906784f,
-                  c3 = 0.055171459913253784f;
-  t.x = fmaxf(t.x, -126.f);
-  t.y = fmaxf(t.y, -126.f);
-  const float2 y = __fadd2_rn(t, make_float2(kMagicF, kMagicF));
-  const float2 n = __fadd2_rn(y, make_float2(-kMagicF, -kMagicF));
-  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), t);
-  float2 p = __ffma2_rn(f, make_float2(c3, c3), make_float2(c2, c2));
-  p = __ffma2_rn(p, f, make_float2(c1, c1));
-  p = __ffma2_rn(p, f, make_float2(c0, c0));
-  return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(y.x) << 23)),
-                     __int_as_float(__float_as_int(p.y) + (__float_as_int(y.y) << 23)));
-}
-
 // Barrier of one 128-thread warpgroup: named barrier `id` (1, 2, ...; 0 is the CTA barrier),
 // counted per thread, so warps may arrive diverged.
 __device__ __forceinline__ void group_sync(int id) { asm volatile("barrier.sync %0, 128;" ::"r"(id) : "memory"); }

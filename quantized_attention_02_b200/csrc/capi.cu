@@ -11,10 +11,12 @@
 #include <cstdint>
 #include <mutex>
 
+#include "attn16_kernels.cuh"
 #include "attn_kernels.cuh"
 #include "prep_kernels.cuh"
 #include "sage_attn.h"
 #include "sparse_kernels.cuh"
+#include "tensor_map.cuh"
 #include "workspace.cuh"
 
 namespace {
@@ -172,6 +174,20 @@ int attn_quantized_impl(const int8_t* q8, const int8_t* k8, const float* sq, con
 }  // namespace
 
 namespace sage {
+
+bool encode_tiled_16bit(CUtensorMap* map, bool bf16, const void* base, int rank, const uint64_t* dims,
+                        const uint64_t* strides, const uint32_t* box) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], unit[5];
+  for (int i = 0; i < rank; ++i) d[i] = dims[i], bx[i] = box[i], unit[i] = 1;
+  for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, bx, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t workspace_alloc(void** p, size_t bytes, cudaStream_t st) {
   constexpr int kMaxDevices = 64;
@@ -518,7 +534,9 @@ int sage_debug_wait_timeout(int* gave_up, void* stream) {
 int sage_last_device_error(void* stream) {
   cudaError_t e;
   const int code = sage::read_and_clear_device_error(static_cast<cudaStream_t>(stream), &e);
-  return code < 0 ? SAGE_ERR_CUDA : code;
+  if (code < 0) return SAGE_ERR_CUDA;
+  const int code16 = sage::read_and_clear_attn16_error(static_cast<cudaStream_t>(stream), &e);
+  return code16 < 0 ? SAGE_ERR_CUDA : code ? code : code16;
 }
 
 

@@ -1,12 +1,17 @@
 // serving.cu -- C ABI of the serving operators declared in include/sage_attn.h: argument checks and
-// launches of the query / key norm with rotation and of the append into a paged cache.
+// launches of the query / key norm with rotation, the append into a paged cache, the attention over
+// it and the cross attention.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
+#include "attn16_kernels.cuh"
 #include "rope_kernels.cuh"
 #include "sage_attn.h"
+#include "tensor_map.cuh"
+#include "workspace.cuh"
 
 namespace {
 
@@ -49,6 +54,79 @@ int check_pages(int num_pages, int page_size) {
 }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA; }
+
+// ---------------------------------------------------------------- 16-bit attention
+int check_attn(int Hq, int Hk, int d, float sm_scale, int dtype) {
+  if (Hk <= 0) return SAGE_ERR_INVALID;
+  const int rc = check_common(Hq, Hk, d, dtype);
+  if (rc) return rc;
+  if (Hq % Hk != 0 || !(std::isfinite(sm_scale) && sm_scale > 0.f)) return SAGE_ERR_INVALID;
+  return Hq / Hk <= 128 ? SAGE_OK : SAGE_ERR_UNSUPPORTED;  // a group's heads are rows of one query tile
+}
+
+// Byte stride of a dimension for a tensor map: any valid value where the extent is 1.
+uint64_t map_stride(int64_t elems, int64_t extent, int d) {
+  return static_cast<uint64_t>(extent > 1 ? elems : d) * 2;
+}
+
+bool strides_fit(const sage_strides* s) {  // 40-bit byte strides
+  return s->b < (1ll << 38) && s->h < (1ll << 31) && s->n < (1ll << 38);
+}
+
+// queries [B][Hk][N][G][d] from a [B][Hq][N][d] view
+bool query_map(CUtensorMap* m, bool bf16, const void* q, const sage_strides& st, int B, int Hk, int G, int N, int d,
+               int tile_tokens) {
+  const uint64_t dims[5] = {static_cast<uint64_t>(d), static_cast<uint64_t>(G), static_cast<uint64_t>(N),
+                            static_cast<uint64_t>(Hk), static_cast<uint64_t>(B)};
+  const uint64_t strides[4] = {map_stride(st.h, G, d), map_stride(st.n, N, d), map_stride(st.h * G, Hk, d),
+                               map_stride(st.b, B, d)};
+  const uint32_t box[5] = {64u, static_cast<uint32_t>(G), static_cast<uint32_t>(tile_tokens), 1u, 1u};
+  return sage::encode_tiled_16bit(m, bf16, q, 5, dims, strides, box);
+}
+
+// keys or values [outer][Hk][rows][d]: outer = batch entries, or a cache's pages
+bool key_map(CUtensorMap* m, bool bf16, const void* k, const sage_strides& st, int outer, int Hk, int rows, int d,
+             int box_rows) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(Hk),
+                            static_cast<uint64_t>(outer)};
+  const uint64_t strides[3] = {map_stride(st.n, rows, d), map_stride(st.h, Hk, d), map_stride(st.b, outer, d)};
+  const uint32_t box[4] = {64u, static_cast<uint32_t>(box_rows), 1u, 1u};
+  return sage::encode_tiled_16bit(m, bf16, k, 4, dims, strides, box);
+}
+
+// Shape of the launch, workspace for the key parts, launch.  l holds the tensors, sizes and maps; the
+// query tiles' shape (pair, slots) follows from `pair`.
+int run_attn16(sage::Attn16Launch& l, int Hq, int64_t ctas, cudaStream_t st) {
+  sage::Attn16Args& a = l.a;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SAGE_ERR_CUDA;
+  // Fewer CTAs than SMs: split the key axis so that each SM has a part, of 512 keys at least.  How many
+  // parts a sequence really has follows on the device from its length.
+  a.min_chunk = 4;
+  const int64_t tiles = (a.Nk + 127ll) / 128;
+  a.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(ctas, 1),
+                                                                     (tiles + a.min_chunk - 1) / a.min_chunk)));
+  if (static_cast<int64_t>(a.slots) * a.splits * a.Hk >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
+  void* ws = nullptr;
+  if (a.splits > 1) {
+    const int64_t rows = static_cast<int64_t>(a.cu_q ? 1 : a.B) * a.Nq * Hq * a.splits;
+    const size_t o_bytes = static_cast<size_t>(rows) * l.D * sizeof(float);
+    if (sage::workspace_alloc(&ws, o_bytes + static_cast<size_t>(rows) * sizeof(float2), st) != cudaSuccess) {
+      cudaGetLastError();
+      return SAGE_ERR_NOMEM;
+    }
+    a.part_o = static_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + o_bytes);
+  }
+  int rc = cuda_status(sage::launch_attn16(l, st));
+  if (ws) {
+    const cudaError_t fe = cudaFreeAsync(ws, st);
+    if (!rc && fe != cudaSuccess) rc = SAGE_ERR_CUDA;
+  }
+  return rc;
+}
 
 }  // namespace
 
@@ -116,6 +194,92 @@ int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* 
   a.interleaved = interleaved != 0;
   a.bf16 = dtype == SAGE_BF16;
   return cuda_status(sage::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, void* o, const sage_strides* q_st,
+                    const sage_strides* k_cache_st, const sage_strides* v_cache_st, const sage_strides* o_st,
+                    const int32_t* page_table, const int32_t* cu_q, const int32_t* kv_len, int B, int T, int Hq,
+                    int Hk, int d, int num_pages, int page_size, int pages_per_seq, int causal, float sm_scale,
+                    int dtype, void* stream) {
+  if (B < 0 || T < 0 || pages_per_seq < 0) return SAGE_ERR_INVALID;
+  int rc = check_attn(Hq, Hk, d, sm_scale, dtype);
+  if (rc) return rc;
+  if ((rc = check_pages(num_pages, page_size))) return rc;
+  if (B == 0 || T == 0) return SAGE_OK;
+  if (!cu_q || !kv_len || (pages_per_seq > 0 && !page_table) || !view_ok(q, q_st, 1, Hq, T) ||
+      !view_ok(o, o_st, 1, Hq, T) || !view_ok(k_cache, k_cache_st, num_pages, Hk, page_size) ||
+      !view_ok(v_cache, v_cache_st, num_pages, Hk, page_size))
+    return SAGE_ERR_INVALID;
+  if (static_cast<int64_t>(pages_per_seq) * page_size >= (1ll << 31) ||
+      static_cast<int64_t>(T) * Hq >= (1ll << 31) || !strides_fit(q_st) || !strides_fit(k_cache_st) ||
+      !strides_fit(v_cache_st))
+    return SAGE_ERR_UNSUPPORTED;
+  const int G = Hq / Hk;
+  sage::Attn16Launch l{};
+  sage::Attn16Args& a = l.a;
+  a.o = o;
+  a.o_sh = o_st->h, a.o_sn = o_st->n;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.page_table = page_table;
+  a.pages_per_seq = pages_per_seq, a.num_pages = num_pages, a.page_shift = page_shift(page_size);
+  a.B = B, a.Nq = T, a.Nk = pages_per_seq * page_size;
+  a.Hk = Hk, a.G = G;
+  a.tile_tokens = 128 / G;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.causal = causal != 0;
+  l.D = d;
+  l.bf16 = dtype == SAGE_BF16;
+  // pairs of query tiles when the average sequence has more rows than one tile holds
+  l.pair = static_cast<int64_t>(T) > static_cast<int64_t>(B) * a.tile_tokens;
+  const int cta_tokens = (l.pair ? 2 : 1) * a.tile_tokens;
+  a.slots = T / cta_tokens + B;
+  if (!query_map(&l.tm_q, l.bf16, q, *q_st, 1, Hk, G, T, d, a.tile_tokens) ||
+      !key_map(&l.tm_k, l.bf16, k_cache, *k_cache_st, num_pages, Hk, page_size, d, std::min(128, page_size)) ||
+      !key_map(&l.tm_v, l.bf16, v_cache, *v_cache_st, num_pages, Hk, page_size, d, std::min(128, page_size)))
+    return SAGE_ERR_CUDA;
+  const int64_t tiles = std::max(std::min(B, T), (T + cta_tokens - 1) / cta_tokens);
+  return run_attn16(l, Hq, tiles * Hk, static_cast<cudaStream_t>(stream));
+}
+
+int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const sage_strides* q_st,
+                    const sage_strides* k_st, const sage_strides* v_st, const sage_strides* o_st,
+                    const int32_t* key_len, int B, int Hq, int Hk, int Nq, int Nk, int d, float sm_scale, int dtype,
+                    void* stream) {
+  if (B < 0 || Nq < 0 || Nk < 0) return SAGE_ERR_INVALID;
+  int rc = check_attn(Hq, Hk, d, sm_scale, dtype);
+  if (rc) return rc;
+  if (B == 0 || Nq == 0) return SAGE_OK;
+  if (!view_ok(q, q_st, B, Hq, Nq) || !view_ok(o, o_st, B, Hq, Nq)) return SAGE_ERR_INVALID;
+  if (Nk > 0 && (!view_ok(k, k_st, B, Hk, Nk) || !view_ok(v, v_st, B, Hk, Nk))) return SAGE_ERR_INVALID;
+  if (static_cast<int64_t>(B) * Nq * Hq >= (1ll << 31) || Nk > (1 << 30) || !strides_fit(q_st) ||
+      (Nk > 0 && (!strides_fit(k_st) || !strides_fit(v_st))))
+    return SAGE_ERR_UNSUPPORTED;
+  const int G = Hq / Hk;
+  sage::Attn16Launch l{};
+  sage::Attn16Args& a = l.a;
+  a.o = o;
+  a.o_sb = o_st->b, a.o_sh = o_st->h, a.o_sn = o_st->n;
+  a.kv_len = Nk > 0 ? key_len : nullptr;
+  a.B = B, a.Nq = Nq, a.Nk = Nk;
+  a.Hk = Hk, a.G = G;
+  a.tile_tokens = 128 / G;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  l.D = d;
+  l.bf16 = dtype == SAGE_BF16;
+  l.pair = Nq > a.tile_tokens;
+  const int cta_tokens = (l.pair ? 2 : 1) * a.tile_tokens;
+  const int64_t slots = static_cast<int64_t>(B) * ((Nq + cta_tokens - 1) / cta_tokens);
+  if (slots >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
+  a.slots = static_cast<int>(slots);
+  if (!query_map(&l.tm_q, l.bf16, q, *q_st, B, Hk, G, Nq, d, a.tile_tokens)) return SAGE_ERR_CUDA;
+  if (Nk > 0) {
+    if (!key_map(&l.tm_k, l.bf16, k, *k_st, B, Hk, Nk, d, 128) || !key_map(&l.tm_v, l.bf16, v, *v_st, B, Hk, Nk, d, 128))
+      return SAGE_ERR_CUDA;
+  } else {
+    l.tm_k = l.tm_v = l.tm_q;  // no key: nothing is loaded, every row is 0
+  }
+  return run_attn16(l, Hq, slots * Hk, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

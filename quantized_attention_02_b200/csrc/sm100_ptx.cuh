@@ -34,15 +34,14 @@ __device__ __forceinline__ long long clock_stamp() {
 namespace sage {
 
 // ---------------------------------------------------------------- status word
-// Written by kernels when a bounded wait gives up; read by sage_last_device_error().
-// Defined here: exactly one translation unit (the one holding the tcgen05 kernels) includes
-// this header.
+// Written by kernels when a bounded wait gives up; read by sage_last_device_error(), which asks
+// every translation unit that includes this header: each has a word of its own.
 enum DeviceError : int {
   kDevOk = 0,
   kDevTimeoutBarrier = 1,
   kDevBarrierEarly = 2,  // trace builds: a CTA barrier let a thread through before all had arrived
 };
-__device__ int g_device_error = 0;
+static __device__ int g_device_error = 0;
 
 constexpr long long kWaitLimitCycles = 1ll << 30;  // ~0.5 s at 2 GHz
 
@@ -130,6 +129,25 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// 4-D and 5-D forms of the load (a paged cache: channel, row in page, head, page; queries: channel,
+// head in group, token, group, batch).
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z, int32_t w, int32_t v) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
       : "memory");
 }
 

@@ -94,3 +94,62 @@ def test_binding_refuses_host_tensors(sa):
 def test_strides_struct_matches_the_header(sa):
     assert ctypes.sizeof(sa.SageStrides) == 24
     assert [n for n, _ in sa.SageStrides._fields_] == ["b", "h", "n"]
+
+
+def paged(sa, **kw):
+    st = strides(sa)
+    a = dict(q=FAKE, kc=FAKE, vc=FAKE, o=FAKE, qs=st, kcs=st, vcs=st, os=st, table=FAKE, cu=FAKE, len=FAKE, B=2, T=8,
+             Hq=4, Hk=2, d=128, pages=4, page=16, width=2, causal=1, scale=0.1, dtype=sa.SAGE_F16, stream=None)
+    a.update(kw)
+    return sa.get_lib().sage_paged_attn(*a.values())
+
+
+def cross(sa, **kw):
+    st = strides(sa)
+    a = dict(q=FAKE, k=FAKE, v=FAKE, o=FAKE, qs=st, ks=st, vs=st, os=st, len=None, B=2, Hq=4, Hk=2, Nq=8, Nk=9, d=128,
+             scale=0.1, dtype=sa.SAGE_F16, stream=None)
+    a.update(kw)
+    return sa.get_lib().sage_cross_attn(*a.values())
+
+
+ATTN_REFUSED = [
+    (dict(q=None), INVALID), (dict(q=ODD), INVALID), (dict(o=None), INVALID), (dict(o=ODD), INVALID),
+    (dict(B=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hk=0), INVALID), (dict(Hk=3), INVALID),
+    (dict(Hq=130, Hk=1), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(d=256), UNSUPPORTED), (dict(dtype=2), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=float("inf")), INVALID),
+]
+
+
+@pytest.mark.parametrize("kw,status", ATTN_REFUSED + [
+    (dict(kc=None), INVALID), (dict(vc=ODD), INVALID), (dict(table=None), INVALID), (dict(cu=None), INVALID),
+    (dict(len=None), INVALID), (dict(T=-1), INVALID), (dict(pages=0), INVALID), (dict(width=-1), INVALID),
+    (dict(page=8), UNSUPPORTED), (dict(page=100), UNSUPPORTED), (dict(page=512), UNSUPPORTED),
+    (dict(width=1 << 27), UNSUPPORTED), (dict(T=1 << 29), UNSUPPORTED),
+], ids=lambda v: str(v))
+def test_paged_attn_refuses(sa, kw, status):
+    assert paged(sa, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", ATTN_REFUSED + [
+    (dict(k=None), INVALID), (dict(v=ODD), INVALID), (dict(Nq=-1), INVALID), (dict(Nk=-1), INVALID),
+    (dict(Nq=1 << 29), UNSUPPORTED), (dict(Nk=(1 << 30) + 1), UNSUPPORTED),
+], ids=lambda v: str(v))
+def test_cross_attn_refuses(sa, kw, status):
+    assert cross(sa, **kw) == status
+
+
+@pytest.mark.parametrize("field,value,status", [("b", 12, INVALID), ("h", 4, INVALID), ("n", 0, INVALID),
+                                                ("n", -128, INVALID), ("b", 1 << 40, UNSUPPORTED)])
+def test_attention_refuses_strides(sa, field, value, status):
+    st = strides(sa)
+    setattr(st, field, value)
+    for name in ("qs", "ks", "vs"):
+        assert cross(sa, **{name: st}) == status
+    for name in ("kcs", "vcs"):
+        assert paged(sa, **{name: st}) == status
+
+
+def test_attention_without_tokens_is_no_work(sa):
+    assert paged(sa, T=0, q=None, o=None) == 0 and paged(sa, B=0, table=None, cu=None, len=None) == 0
+    assert cross(sa, Nq=0, q=None, o=None) == 0 and cross(sa, B=0) == 0
