@@ -30,6 +30,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "attn16_device.cuh"
 #include "attn16_kernels.cuh"
 #include "attn_common.cuh"
 #include "sm100_ptx.cuh"
@@ -74,32 +75,9 @@ __device__ __forceinline__ KeyRange key_range(int nt, int splits, int min_chunk,
   return r;
 }
 
-struct Sequence {
-  int b, token0, nq, kv;  // token0: first token in the query tensor (paged) or 0 (dense)
-};
-
-__device__ __forceinline__ int keys_of(const Attn16Args& a, int b) {
-  return a.kv_len ? min(max(__ldg(a.kv_len + b), 0), a.Nk) : a.Nk;
-}
-
-// Keys that query `tok` of the sequence sees.
-__device__ __forceinline__ int visible(const Attn16Args& a, const Sequence& s, int tok) {
-  return a.causal ? min(max(s.kv - s.nq + tok + 1, 0), s.kv) : s.kv;
-}
-
 // Key tiles the CTA's query tiles see together: those of the last token.
 __device__ __forceinline__ int key_tiles(const Attn16Args& a, const Sequence& s, int tok0, int cta_tokens) {
   return (visible(a, s, min(s.nq, tok0 + cta_tokens) - 1) + 127) / 128;
-}
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    return pack_half2(lo, hi);
-  }
 }
 
 template <int D, bool BF16, int NQT>

@@ -1,5 +1,5 @@
-// attn16_kernels.cuh -- launcher of the 16-bit attention kernel (attn16_kernels.cu) behind the paged
-// attention and the cross attention.
+// attn16_kernels.cuh -- launchers of the 16-bit attention kernels behind the paged attention and the cross
+// attention: attn16_kernels.cu (tiles of query rows) and attn_step_kernels.cu (few rows).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -37,6 +37,25 @@ struct Attn16Launch {
 };
 
 cudaError_t launch_attn16(const Attn16Launch& l, cudaStream_t st);
+
+// The same for few query rows (attn_step_kernels.cu): items of at most kStepRows rows, tile_tokens =
+// kStepRows / G tokens.  Of a, slots, splits and min_chunk are not used; part_o and part_ml hold
+// step_part_rows(ctas) rows.
+constexpr int kStepRows = 16;
+struct StepArgs {
+  Attn16Args a;
+  int tile_tokens;
+};
+struct StepLaunch {
+  StepArgs s;
+  CUtensorMap tm_q, tm_k, tm_v;  // as Attn16Launch, the q box with this tile_tokens
+  int D;
+  bool bf16;
+};
+int step_ctas(const StepArgs& s, int sms);
+size_t step_part_rows(int ctas);
+cudaError_t launch_attn_step(const StepLaunch& l, int ctas, cudaStream_t st);
+int read_and_clear_step_error(cudaStream_t st, cudaError_t* err);
 int read_and_clear_attn16_error(cudaStream_t st, cudaError_t* err);
 
 }  // namespace sage

@@ -536,7 +536,10 @@ int sage_last_device_error(void* stream) {
   const int code = sage::read_and_clear_device_error(static_cast<cudaStream_t>(stream), &e);
   if (code < 0) return SAGE_ERR_CUDA;
   const int code16 = sage::read_and_clear_attn16_error(static_cast<cudaStream_t>(stream), &e);
-  return code16 < 0 ? SAGE_ERR_CUDA : code ? code : code16;
+  if (code16 < 0) return SAGE_ERR_CUDA;
+  const int code_step = sage::read_and_clear_step_error(static_cast<cudaStream_t>(stream), &e);
+  if (code_step < 0) return SAGE_ERR_CUDA;
+  return code ? code : code16 ? code16 : code_step;
 }
 
 

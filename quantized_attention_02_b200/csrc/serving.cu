@@ -94,39 +94,67 @@ bool key_map(CUtensorMap* m, bool bf16, const void* k, const sage_strides& st, i
   return sage::encode_tiled_16bit(m, bf16, k, 4, dims, strides, box);
 }
 
-// Shape of the launch, workspace for the key parts, launch.  l holds the tensors, sizes and maps; the
-// query tiles' shape (pair, slots) follows from `pair`.
-int run_attn16(sage::Attn16Launch& l, int Hq, int64_t ctas, cudaStream_t st) {
-  sage::Attn16Args& a = l.a;
+int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return SAGE_ERR_CUDA;
-  // Fewer CTAs than SMs: split the key axis so that each SM has a part, of 512 keys at least.  How many
-  // parts a sequence really has follows on the device from its length.
+    return 0;
+  return sms;
+}
+
+// fp32 parts of `rows` rows: O, then (m, l).  Stream-ordered, freed by part_free.
+int part_alloc(sage::Attn16Args& a, void** ws, int64_t rows, int d, cudaStream_t st) {
+  const size_t o_bytes = static_cast<size_t>(rows) * d * sizeof(float);
+  if (sage::workspace_alloc(ws, o_bytes + static_cast<size_t>(rows) * sizeof(float2), st) != cudaSuccess) {
+    cudaGetLastError();
+    return SAGE_ERR_NOMEM;
+  }
+  a.part_o = static_cast<float*>(*ws);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(*ws) + o_bytes);
+  return SAGE_OK;
+}
+int part_free(void* ws, int rc, cudaStream_t st) {
+  if (!ws) return rc;
+  const cudaError_t fe = cudaFreeAsync(ws, st);
+  return !rc && fe != cudaSuccess ? SAGE_ERR_CUDA : rc;
+}
+
+// Few rows: one axis of key units over all sequences, cut into equal shares.
+int run_step(const sage::Attn16Launch& t, cudaStream_t st) {
+  const int sms = sm_count();
+  if (sms <= 0) return SAGE_ERR_CUDA;
+  sage::StepLaunch l{{t.a, t.a.tile_tokens}, t.tm_q, t.tm_k, t.tm_v, t.D, t.bf16};
+  const int ctas = sage::step_ctas(l.s, sms);
+  void* ws = nullptr;
+  int rc = SAGE_OK;
+  if (ctas > 1 && (rc = part_alloc(l.s.a, &ws, static_cast<int64_t>(sage::step_part_rows(ctas)), l.D, st))) return rc;
+  return part_free(ws, cuda_status(sage::launch_attn_step(l, ctas, st)), st);
+}
+
+// Tiles of query rows.  Fewer CTAs than SMs: the key axis is split so that each SM has a part, of 512 keys
+// at least.  How many parts a sequence really has follows on the device from its length.
+int run_attn16(sage::Attn16Launch& l, int Hq, int64_t ctas, cudaStream_t st) {
+  sage::Attn16Args& a = l.a;
+  const int sms = sm_count();
+  if (sms <= 0) return SAGE_ERR_CUDA;
   a.min_chunk = 4;
   const int64_t tiles = (a.Nk + 127ll) / 128;
   a.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(ctas, 1),
                                                                      (tiles + a.min_chunk - 1) / a.min_chunk)));
   if (static_cast<int64_t>(a.slots) * a.splits * a.Hk >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
   void* ws = nullptr;
-  if (a.splits > 1) {
-    const int64_t rows = static_cast<int64_t>(a.cu_q ? 1 : a.B) * a.Nq * Hq * a.splits;
-    const size_t o_bytes = static_cast<size_t>(rows) * l.D * sizeof(float);
-    if (sage::workspace_alloc(&ws, o_bytes + static_cast<size_t>(rows) * sizeof(float2), st) != cudaSuccess) {
-      cudaGetLastError();
-      return SAGE_ERR_NOMEM;
-    }
-    a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + o_bytes);
-  }
-  int rc = cuda_status(sage::launch_attn16(l, st));
-  if (ws) {
-    const cudaError_t fe = cudaFreeAsync(ws, st);
-    if (!rc && fe != cudaSuccess) rc = SAGE_ERR_CUDA;
-  }
-  return rc;
+  int rc = SAGE_OK;
+  if (a.splits > 1 &&
+      (rc = part_alloc(a, &ws, static_cast<int64_t>(a.cu_q ? 1 : a.B) * a.Nq * Hq * a.splits, l.D, st)))
+    return rc;
+  return part_free(ws, cuda_status(sage::launch_attn16(l, st)), st);
 }
+
+// Which kernel: by the rows (tokens x group) that a key head of an average sequence has.
+bool few_rows(int64_t tokens, int64_t sequences, int G) {
+  return G <= sage::kStepRows && tokens * G <= sequences * sage::kStepRows;
+}
+constexpr int kTileRows = 128;  // one query tile
 
 }  // namespace
 
@@ -225,19 +253,21 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
   a.pages_per_seq = pages_per_seq, a.num_pages = num_pages, a.page_shift = page_shift(page_size);
   a.B = B, a.Nq = T, a.Nk = pages_per_seq * page_size;
   a.Hk = Hk, a.G = G;
-  a.tile_tokens = 128 / G;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.causal = causal != 0;
   l.D = d;
   l.bf16 = dtype == SAGE_BF16;
-  // pairs of query tiles when the average sequence has more rows than one tile holds
-  l.pair = static_cast<int64_t>(T) > static_cast<int64_t>(B) * a.tile_tokens;
-  const int cta_tokens = (l.pair ? 2 : 1) * a.tile_tokens;
-  a.slots = T / cta_tokens + B;
+  const bool step = few_rows(T, B, G) && static_cast<int64_t>(B) * Hk < (1ll << 31);
+  a.tile_tokens = (step ? sage::kStepRows : kTileRows) / G;
   if (!query_map(&l.tm_q, l.bf16, q, *q_st, 1, Hk, G, T, d, a.tile_tokens) ||
       !key_map(&l.tm_k, l.bf16, k_cache, *k_cache_st, num_pages, Hk, page_size, d, std::min(128, page_size)) ||
       !key_map(&l.tm_v, l.bf16, v_cache, *v_cache_st, num_pages, Hk, page_size, d, std::min(128, page_size)))
     return SAGE_ERR_CUDA;
+  if (step) return run_step(l, static_cast<cudaStream_t>(stream));
+  // pairs of query tiles when the average sequence has more rows than one tile holds
+  l.pair = static_cast<int64_t>(T) * G > static_cast<int64_t>(B) * kTileRows;
+  const int cta_tokens = (l.pair ? 2 : 1) * a.tile_tokens;
+  a.slots = T / cta_tokens + B;
   const int64_t tiles = std::max(std::min(B, T), (T + cta_tokens - 1) / cta_tokens);
   return run_attn16(l, Hq, tiles * Hk, static_cast<cudaStream_t>(stream));
 }
@@ -263,15 +293,11 @@ int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const 
   a.kv_len = Nk > 0 ? key_len : nullptr;
   a.B = B, a.Nq = Nq, a.Nk = Nk;
   a.Hk = Hk, a.G = G;
-  a.tile_tokens = 128 / G;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   l.D = d;
   l.bf16 = dtype == SAGE_BF16;
-  l.pair = Nq > a.tile_tokens;
-  const int cta_tokens = (l.pair ? 2 : 1) * a.tile_tokens;
-  const int64_t slots = static_cast<int64_t>(B) * ((Nq + cta_tokens - 1) / cta_tokens);
-  if (slots >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
-  a.slots = static_cast<int>(slots);
+  const bool step = few_rows(Nq, 1, G) && static_cast<int64_t>(B) * Hk < (1ll << 31);
+  a.tile_tokens = (step ? sage::kStepRows : kTileRows) / G;
   if (!query_map(&l.tm_q, l.bf16, q, *q_st, B, Hk, G, Nq, d, a.tile_tokens)) return SAGE_ERR_CUDA;
   if (Nk > 0) {
     if (!key_map(&l.tm_k, l.bf16, k, *k_st, B, Hk, Nk, d, 128) || !key_map(&l.tm_v, l.bf16, v, *v_st, B, Hk, Nk, d, 128))
@@ -279,6 +305,12 @@ int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const 
   } else {
     l.tm_k = l.tm_v = l.tm_q;  // no key: nothing is loaded, every row is 0
   }
+  if (step) return run_step(l, static_cast<cudaStream_t>(stream));
+  l.pair = Nq > a.tile_tokens;
+  const int cta_tokens = (l.pair ? 2 : 1) * a.tile_tokens;
+  const int64_t slots = static_cast<int64_t>(B) * ((Nq + cta_tokens - 1) / cta_tokens);
+  if (slots >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
+  a.slots = static_cast<int>(slots);
   return run_attn16(l, Hq, slots * Hk, static_cast<cudaStream_t>(stream));
 }
 

@@ -40,6 +40,10 @@ def check(o, q, k, v, lengths, sm_scale):
     (1, 2, 2, 257, 9000, 128, None),             # few tiles, long states: split with pairs of tiles
     (20, 32, 8, 1, 2500, 128, None),             # more CTAs than SMs, no split: long walks through the rings
     (40, 16, 8, 1, 5001, 64, None),
+    (20, 16, 8, 40, 2500, 128, None),            # one query tile per sequence: 80 rows
+    (25, 12, 6, 33, 3001, 64, None),
+    (3, 5, 1, 3, 1000, 128, [1000, 0, 17]),      # fifteen rows of five heads
+    (300, 2, 1, 2, 70, 64, None),                # many short sequences
     (2, 32, 16, 700, 4100, 128, None),
     (2, 128, 1, 3, 300, 64, [300, 17]),          # the widest group: one token per tile
     (1, 96, 1, 5, 700, 128, None),

@@ -83,6 +83,11 @@ SEQS = {
     "more_new_than_keys": [(40, 10), (300, 150), (5, 0)],
     "many_long_steps": [(1, 6000 - 100 * i) for i in range(40)] * 2,
     "long_chunks": [(200, 3000), (150, 5000), (1, 4000)] * 6,
+    "long_speculative": [(30, 3000)] * 20 + [(1, 2000)] * 5,
+    "two_or_three": [(2, 900), (3, 1500), (0, 10), (1, 3), (2, 1)] * 3,
+    "one_chunk_among_none": [(0, 100)] * 30 + [(29, 800)] + [(0, 5)] * 10,
+    "idle": [(0, 100), (0, 0)],
+    "many_steps": [(1, 1 + 53 * i % 900) for i in range(700)],
     "many": [(1 + i % 3, 1 + 37 * i % 400) for i in range(500)],
 }
 
