@@ -15,7 +15,7 @@
 //
 // CTA organisation (one per SM: 512 TMEM columns, about 226 KB of shared memory), 12 warps:
 //   warp 0      TMA producer: Q once, then K and V tiles of 128 keys through rings, K0 V0 K1 V1 ...
-//   warps 1, 2  MMA issuers of streams 0 and 1 (warp 1 also allocates TMEM)
+//   warp 1      MMA issuer of both streams; allocates TMEM
 //   warps 4-7   softmax of stream 0 (thread = query row = TMEM lane), warps 8-11 of stream 1
 // NQT = 2: the streams are two query tiles that share each key tile.  NQT = 1: one query tile, stream t
 // takes every other key tile, and the two (m, l, O) are joined at the end: single tokens and short
@@ -52,7 +52,7 @@ struct Layout16 {
   static constexpr int OFF_RING = NQT * TILE;
   static constexpr int OFF_ML = OFF_RING + RINGS * NS * TILE;  // [128] (m, l) of stream 1 (NQT = 1)
   static constexpr int OFF_BAR = OFF_ML + 128 * 8;
-  static constexpr int NUM_BARS = 1 + 2 * RINGS * NS + 5 * 2;
+  static constexpr int NUM_BARS = 1 + 2 * RINGS * NS + 4 * 2 + 1;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 384;
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_p_lo = bar_s_full + 2;    // [2] weights of keys 0..63 written
   uint64_t* bar_p_hi = bar_p_lo + 2;      // [2] weights of keys 64..127 written
   uint64_t* bar_o_done = bar_p_hi + 2;    // [2] the stream's last product done
-  uint64_t* bar_drain = bar_o_done + 2;   // [2] the stream's MMAs done at exit
+  uint64_t* bar_drain = bar_o_done + 2;   // all MMAs done at exit
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
@@ -160,18 +160,17 @@ __global__ void __launch_bounds__(384, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(bar_q, 1);
-    const int users = NQT == 2 ? (n_iter[0] > 0) + (n_iter[1] > 0) : 1;
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(bar_full + s, 1);
-      mbar_init(bar_empty + s, max(users, 1));
+      mbar_init(bar_empty + s, 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_s_full + t, 1);
       mbar_init(bar_p_lo + t, 128);
       mbar_init(bar_p_hi + t, 128);
       mbar_init(bar_o_done + t, 1);
-      mbar_init(bar_drain + t, 1);
     }
+    mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
@@ -256,51 +255,58 @@ __global__ void __launch_bounds__(384, 1)
         for (int g = 0; g < L::RINGS; ++g)
           for (int f = max(0, issued[g] - NS); f < issued[g]; ++f) mbar_drain(bar_full + stage(g, f), (f / NS) & 1);
       }
-    } else if (warp == 1 || warp == 2) {
-      // ============================================================ MMA issuers
-      const int t = warp - 1;
-      if (n_iter[t] > 0) {
-        constexpr uint32_t FMT = BF16 ? 1u : 0u;
-        constexpr uint32_t IDESC_QK = make_idesc(1 /*f32*/, FMT, FMT, 0, 0, 128, 128);
-        constexpr uint32_t IDESC_PV = make_idesc(1 /*f32*/, FMT, FMT, 0, 1 /*V is MN-major*/, 128, D);
-        const uint32_t q_base = smem_u32(sQ) + (NQT == 2 ? t * L::TILE : 0), ring = smem_u32(sRing);
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-          return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
-        };
-        auto full = [&](int fill) { return wait(bar_full + stage(t, fill), (fill / NS) & 1); };
-        auto issue_qk = [&](int fill) {
-          const uint32_t k_base = ring + stage(t, fill) * L::TILE;
+    } else if (warp == 1 && n_kv > 0) {
+      // ============================================================ MMA issuer of both streams, in turn: the
+      // second product of one and its next scores, then the other's.  The tensor core so finishes one
+      // stream's scores a whole turn before the other's, and the streams' softmax work falls into each
+      // other's product time.  (Issued by a warp per stream, the products of both finish together, the
+      // softmax warps work at the same time and wait at the same time: 4470 cycles a turn of two 128 x 128
+      // tiles instead of XXXX.)
+      constexpr uint32_t FMT = BF16 ? 1u : 0u;
+      constexpr uint32_t IDESC_QK = make_idesc(1 /*f32*/, FMT, FMT, 0, 0, 128, 128);
+      constexpr uint32_t IDESC_PV = make_idesc(1 /*f32*/, FMT, FMT, 0, 1 /*V is MN-major*/, 128, D);
+      const uint32_t ring = smem_u32(sRing);
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
+      };
+      auto full = [&](int t, int fill) { return wait(bar_full + stage(t, fill), (fill / NS) & 1); };
+      // the last of the streams that read key tile `it` of a shared ring frees its stages
+      auto last_user = [&](int t, int it) { return NQT == 1 || t == 1 || it >= n_iter[1]; };
+      auto issue_qk = [&](int t, int it) {
+        const uint32_t q_base = smem_u32(sQ) + (NQT == 2 ? t * L::TILE : 0);
+        const uint32_t k_base = ring + stage(t, 2 * it) * L::TILE;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {  // 16 channels: 32 bytes inside a 128-byte swizzled row
-            const uint32_t off = (kk / 4) * L::BOX + (kk % 4) * 32;
-            mma_f16_ss_warp(tmem + s_col(t), make_smem_desc(q_base + off, 16, 1024, kSwizzle128B),
-                            make_smem_desc(k_base + off, 16, 1024, kSwizzle128B), IDESC_QK, kk > 0 ? 1u : 0u);
-          }
-          mma_commit_warp(bar_empty + stage(t, fill));
-          mma_commit_warp(bar_s_full + t);
-        };
-        auto issue_pv = [&](int fill, bool first, int k0) {  // 64 keys, 16 per MMA
-          const uint32_t v_base = ring + stage(t, fill) * L::TILE;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kk = k0 / 16 + i;
-            mma_f16_ts_warp(tmem + o_col(t), tmem + s_col(t) + kk * 8,
-                            make_smem_desc(v_base + kk * 16 * 128, L::BOX, 1024, kSwizzle128B), IDESC_PV,
-                            first && kk == 0 ? 0u : 1u);
-          }
-        };
-        bool ok = wait(bar_q, 0) && full(0);
-        if (ok) {
-          tc_fence_after();
-          issue_qk(0);
-        }
-        for (int it = 0; ok && it < n_iter[t]; ++it) {
+        for (int c = 0; c < NB; ++c)  // 16 channels per product: 32 bytes inside a 128-byte swizzled row
+          mma_f16_ss_x4_warp<2, 2>(tmem + s_col(t), make_smem_desc(q_base + c * L::BOX, 16, 1024, kSwizzle128B),
+                                   make_smem_desc(k_base + c * L::BOX, 16, 1024, kSwizzle128B), IDESC_QK, c > 0 ? 1u : 0u);
+        if (last_user(t, it)) mma_commit_warp(bar_empty + stage(t, 2 * it));
+        mma_commit_warp(bar_s_full + t);
+      };
+      auto issue_pv = [&](int t, int it, int half) {  // 64 keys, 16 per MMA
+        const uint32_t v_base = ring + stage(t, 2 * it + 1) * L::TILE;
+        mma_f16_ts_x4_warp<8, 16 * 128 / 16>(tmem + o_col(t), tmem + s_col(t) + half * 32,
+                                             make_smem_desc(v_base + half * 64 * 128, L::BOX, 1024, kSwizzle128B),
+                                             IDESC_PV, it == 0 && half == 0 ? 0u : 1u);
+      };
+      bool ok = wait(bar_q, 0);
+      for (int t = 0; ok && t < 2; ++t) {
+        if (n_iter[t] == 0) continue;
+        if (!full(t, 0)) { ok = false; break; }
+        tc_fence_after();
+        issue_qk(t, 0);
+      }
+      const int steps = max(n_iter[0], n_iter[1]);
+      for (int it = 0; ok && it < steps; ++it) {
+        for (int t = 0; t < 2; ++t) {
+          if (it >= n_iter[t]) continue;
           const int fill = 2 * it + 1;
-          if (!full(fill)) break;
+          // (a shared ring's tile has been waited for in the first stream's turn)
+          const bool seen = NQT == 2 && t == 1 && it < n_iter[0];
+          if (!seen && !full(t, fill)) { ok = false; break; }
           // keys past the sequence's end have no weight, but what stands in their rows (stale or
-          // unwritten memory) may be NaN or infinite: zero those V rows before the product reads them
+          // unwritten memory) may be NaN or infinite: zero those V rows before a product reads them
           const int valid = seq.kv - (range.first + tile_of(t, it)) * 128;
-          if (valid < 128) {
+          if (valid < 128 && !seen) {
             for (int i = lane; i < (128 - valid) * 8 * NB; i += 32) {
               const int c = i / ((128 - valid) * 8), in_box = i % ((128 - valid) * 8);
               *reinterpret_cast<uint4*>(sRing + stage(t, fill) * L::TILE + c * L::BOX + valid * 128 + in_box * 16) =
@@ -309,35 +315,25 @@ __global__ void __launch_bounds__(384, 1)
             fence_proxy_async_shared();
             __syncwarp();
           }
-          if (!wait(bar_p_lo + t, it & 1)) break;
+          if (!wait(bar_p_lo + t, it & 1)) { ok = false; break; }
           tc_fence_after();
-          issue_pv(fill, it == 0, 0);
-          if (!wait(bar_p_hi + t, it & 1)) break;
+          issue_pv(t, it, 0);
+          if (!wait(bar_p_hi + t, it & 1)) { ok = false; break; }
           tc_fence_after();
-          issue_pv(fill, false, 64);
-          mma_commit_warp(bar_empty + stage(t, fill));
+          issue_pv(t, it, 1);
+          if (last_user(t, it)) mma_commit_warp(bar_empty + stage(t, fill));
           if (it + 1 < n_iter[t]) {
-            if (!full(fill + 1)) break;
+            if (!(NQT == 2 && t == 1 && it + 1 < n_iter[0]) && !full(t, fill + 1)) { ok = false; break; }
             tc_fence_after();
-            issue_qk(fill + 1);
+            issue_qk(t, it + 1);
           } else {
             mma_commit_warp(bar_o_done + t);
           }
         }
-        if constexpr (NQT == 2) {
-          // key tiles that only the other stream uses (causal: it sees further) still need this one's
-          // arrival for their stage to be refilled
-          for (int j = n_iter[t]; j < n_kv; ++j) {
-            for (int kind = 0; kind < 2; ++kind) {
-              if (!full(2 * j + kind)) { j = n_kv; break; }
-              if (lane == 0) mbar_arrive(bar_empty + stage(t, 2 * j + kind));
-            }
-          }
-        }
-        // all MMAs issued by this warp must finish before TMEM is released
-        mma_commit_warp(bar_drain + t);
-        mbar_drain(bar_drain + t, 0);
       }
+      // all MMAs must finish before TMEM is released
+      mma_commit_warp(bar_drain);
+      mbar_drain(bar_drain, 0);
     }
   } else {
     reg_alloc<216>();
@@ -375,29 +371,25 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
         for (int c = 0; c < 128; ++c) x[c] = c < seen ? x[c] : 0xFF800000u;
       }
-      float mx4[4];
+      auto row_max = [&]() {  // log2 units
+        float mx[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[4 + k]));
+        for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[8 + k]));
 #pragma unroll
-      for (int c = 8; c < 128; c += 8) {
+        for (int c = 16; c < 128; c += 16) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mx4[k] = max3f(mx4[k], __uint_as_float(x[c + k]), __uint_as_float(x[c + 4 + k]));
-      }
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * a.scale_log2;
-
-      bool rescale = false;
-      float alpha = 1.f;
-      if (it == 0) {
-        m_use = mx;
-      } else if (mx > m_use + 8.f) {  // also the first finite maximum after fully masked tiles
-        alpha = fast_exp2(m_use - mx);
-        m_use = mx;
-        rescale = true;
-      }
-      // every earlier product of the stream is complete (they precede this S), and the next one waits
-      // for the arrivals below: O may be rescaled here
-      if (__any_sync(0xffffffffu, rescale)) {
+          for (int k = 0; k < 8; ++k)
+            mx[k] = max3f(mx[k], __uint_as_float(x[c + k]), __uint_as_float(x[c + 8 + k]));
+        }
+        return fmaxf(max3f(mx[0], mx[1], mx[2]), fmaxf(max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * a.scale_log2;
+      };
+      // The offset moves when the maximum has passed it by 8 (also at the first finite maximum).  Every
+      // earlier product of the stream is complete then (they precede this S), and the next one waits for
+      // the arrivals below: O may be rescaled here.
+      auto move_offset = [&](float mx) {
+        const bool move = mx > m_use + 8.f;
+        const float alpha = move ? fast_exp2(m_use - mx) : 1.f;
+        if (move) m_use = mx;
 #pragma unroll
         for (int i = 0; i < 4; ++i) lsum[i] = __fmul2_rn(lsum[i], make_float2(alpha, alpha));
 #pragma unroll
@@ -408,34 +400,60 @@ __global__ void __launch_bounds__(384, 1)
           for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
           tmem_st32(tO + cb, ov);
         }
-      }
-      const float off = kShift - (m_use == -INFINITY ? 0.f : m_use);
-      const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), off2 = make_float2(off, off);
-      // masked weights are exactly 0 on the MUFU pipe (ex2(-inf)); the polynomial bottoms out at 2^-126
-      // instead, so tiles with masked keys do not use it
-      auto weights = [&](auto poly) {
+      };
+      // Weights of 64 keys into TMEM.  Masked weights are exactly 0 on the MUFU pipe (ex2(-inf)); the
+      // polynomial bottoms out at 2^-126 instead, so tiles with masked keys do not use it.
+      auto weights = [&](int half, auto poly, float2 (&sum)[4]) {
+        const float off = kShift - (m_use == -INFINITY ? 0.f : m_use);
+        const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), off2 = make_float2(off, off);
 #pragma unroll
-        for (int cb = 0; cb < 128; cb += 32) {
+        for (int cb = 0; cb < 64; cb += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[cb + i]), __uint_as_float(x[cb + i + 1])), sc2, off2);
+            const int c = 64 * half + cb + i;
+            const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, off2);
             float2 p;
             if (decltype(poly)::value && ((i >> 1) & 3) == 3) p = exp2_poly2(u);
             else p = make_float2(fast_exp2(u.x), fast_exp2(u.y));
-            lsum[(i >> 1) & 3] = __fadd2_rn(lsum[(i >> 1) & 3], p);
+            sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
             pk[i >> 1] = pack16<BF16>(p.x, p.y);
           }
-          tmem_st16(tS + (cb >> 1), pk);
-          if (cb == 32 || cb == 96) {
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(cb == 32 ? bar_p_lo + t : bar_p_hi + t);
-          }
+          tmem_st16(tS + 32 * half + (cb >> 1), pk);
         }
       };
-      if (masked) weights(std::false_type{});
-      else weights(std::true_type{});
+      auto publish = [&](int half) {
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(half == 0 ? bar_p_lo + t : bar_p_hi + t);
+      };
+      if (it == 0 || masked) {
+        const float mx = row_max();
+        if (it == 0) m_use = mx;
+        else if (__any_sync(0xffffffffu, mx > m_use + 8.f)) move_offset(mx);
+        weights(0, std::false_type{}, lsum);
+        publish(0);
+        weights(1, std::false_type{}, lsum);
+        publish(1);
+      } else {
+        // The offset hardly ever moves after the first tiles: the first 64 weights are taken at the old
+        // one while the maximum is found beside them, and taken again if it did move.
+        float2 sum[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = lsum[i];
+        weights(0, std::true_type{}, sum);
+        const float mx = row_max();
+        if (__any_sync(0xffffffffu, mx > m_use + 8.f)) {
+          move_offset(mx);
+          weights(0, std::true_type{}, lsum);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) lsum[i] = sum[i];
+        }
+        publish(0);
+        weights(1, std::true_type{}, lsum);
+        publish(1);
+      }
     }
 
     // ---- epilogue
