@@ -53,6 +53,9 @@ struct Layout16 {
   static constexpr int OFF_ML = OFF_RING + RINGS * NS * TILE;  // [128] (m, l) of stream 1 (NQT = 1)
   static constexpr int OFF_BAR = OFF_ML + 128 * 8;
   static constexpr int NUM_BARS = 1 + 2 * RINGS * NS + 4 * 2 + 1;
+  // d = 64 leaves TMEM columns for the weights beside the scores, so that the next scores can be computed as
+  // soon as these are in registers
+  static constexpr bool OWN_P = D == 64;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
   static constexpr int THREADS = 384;
@@ -97,10 +100,10 @@ __global__ void __launch_bounds__(384, 1)
   uint64_t* bar_full = bar_q + 1;
   uint64_t* bar_empty = bar_full + STAGES;
   uint64_t* bar_s_full = bar_empty + STAGES;  // [2] S_t of the next key tile (and every product before it) done
-  uint64_t* bar_p_lo = bar_s_full + 2;    // [2] weights of keys 0..63 written
-  uint64_t* bar_p_hi = bar_p_lo + 2;      // [2] weights of keys 64..127 written
-  uint64_t* bar_o_done = bar_p_hi + 2;    // [2] the stream's last product done
-  uint64_t* bar_drain = bar_o_done + 2;   // all MMAs done at exit
+  uint64_t* bar_s_free = bar_s_full + 2;  // [2] S_t is in registers (OWN_P)
+  uint64_t* bar_p_full = bar_s_free + 2;  // [2] the tile's weights written
+  uint64_t* bar_pv = bar_p_full + 2;      // [2] the tile's second product done (OWN_P; else: the last tile's)
+  uint64_t* bar_drain = bar_pv + 2;       // all MMAs done at exit
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
 
@@ -166,9 +169,9 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_s_full + t, 1);
-      mbar_init(bar_p_lo + t, 128);
-      mbar_init(bar_p_hi + t, 128);
-      mbar_init(bar_o_done + t, 1);
+      mbar_init(bar_s_free + t, 128);
+      mbar_init(bar_p_full + t, 128);
+      mbar_init(bar_pv + t, 1);
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
@@ -187,6 +190,7 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem = *tmem_slot;
   auto s_col = [](int t) { return 128u * t; };
   auto o_col = [](int t) { return 256u + static_cast<uint32_t>(D) * t; };
+  auto p_col = [&](int t) { return L::OWN_P ? 384u + 64u * t : s_col(t); };
 
   // Registers: launched with 168 per thread (384 x 168); 128 x 72 + 256 x 216 is the same total.  Each
   // setmaxnreg is executed by a whole warpgroup and dominates that group's code.
@@ -259,9 +263,9 @@ __global__ void __launch_bounds__(384, 1)
       // ============================================================ MMA issuer of both streams, in turn: the
       // second product of one and its next scores, then the other's.  The tensor core so finishes one
       // stream's scores a whole turn before the other's, and the streams' softmax work falls into each
-      // other's product time.  (Issued by a warp per stream, the products of both finish together, the
+      // other's product time.  (Issued by a warp per stream, the products of both finish together and the
       // softmax warps work at the same time and wait at the same time: 4470 cycles a turn of two 128 x 128
-      // tiles instead of XXXX.)
+      // tiles of d = 128 instead of 3330.)  The whole warp runs the loop; see mma_f16_ss_x4_warp.
       constexpr uint32_t FMT = BF16 ? 1u : 0u;
       constexpr uint32_t IDESC_QK = make_idesc(1 /*f32*/, FMT, FMT, 0, 0, 128, 128);
       constexpr uint32_t IDESC_PV = make_idesc(1 /*f32*/, FMT, FMT, 0, 1 /*V is MN-major*/, 128, D);
@@ -270,64 +274,64 @@ __global__ void __launch_bounds__(384, 1)
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
       };
       auto full = [&](int t, int fill) { return wait(bar_full + stage(t, fill), (fill / NS) & 1); };
-      // the last of the streams that read key tile `it` of a shared ring frees its stages
+      // a shared ring's tile `it` is waited for in its first stream's turn and freed in its last one's
+      auto first_user = [&](int t, int it) { return NQT == 1 || t == 0 || it >= n_iter[0]; };
       auto last_user = [&](int t, int it) { return NQT == 1 || t == 1 || it >= n_iter[1]; };
-      auto issue_qk = [&](int t, int it) {
+      auto issue_qk = [&](int t, int it) -> bool {
+        if (first_user(t, it) && !full(t, 2 * it)) return false;
+        if (L::OWN_P && it > 0 && !wait(bar_s_free + t, (it - 1) & 1)) return false;
+        tc_fence_after();
         const uint32_t q_base = smem_u32(sQ) + (NQT == 2 ? t * L::TILE : 0);
         const uint32_t k_base = ring + stage(t, 2 * it) * L::TILE;
 #pragma unroll
         for (int c = 0; c < NB; ++c)  // 16 channels per product: 32 bytes inside a 128-byte swizzled row
           mma_f16_ss_x4_warp<2, 2>(tmem + s_col(t), make_smem_desc(q_base + c * L::BOX, 16, 1024, kSwizzle128B),
                                    make_smem_desc(k_base + c * L::BOX, 16, 1024, kSwizzle128B), IDESC_QK, c > 0 ? 1u : 0u);
-        if (last_user(t, it)) mma_commit_warp(bar_empty + stage(t, 2 * it));
         mma_commit_warp(bar_s_full + t);
+        if (last_user(t, it)) mma_commit_warp(bar_empty + stage(t, 2 * it));
+        return true;
       };
-      auto issue_pv = [&](int t, int it, int half) {  // 64 keys, 16 per MMA
-        const uint32_t v_base = ring + stage(t, 2 * it + 1) * L::TILE;
-        mma_f16_ts_x4_warp<8, 16 * 128 / 16>(tmem + o_col(t), tmem + s_col(t) + half * 32,
-                                             make_smem_desc(v_base + half * 64 * 128, L::BOX, 1024, kSwizzle128B),
-                                             IDESC_PV, it == 0 && half == 0 ? 0u : 1u);
-      };
-      bool ok = wait(bar_q, 0);
-      for (int t = 0; ok && t < 2; ++t) {
-        if (n_iter[t] == 0) continue;
-        if (!full(t, 0)) { ok = false; break; }
-        tc_fence_after();
-        issue_qk(t, 0);
-      }
-      const int steps = max(n_iter[0], n_iter[1]);
-      for (int it = 0; ok && it < steps; ++it) {
-        for (int t = 0; t < 2; ++t) {
-          if (it >= n_iter[t]) continue;
-          const int fill = 2 * it + 1;
-          // (a shared ring's tile has been waited for in the first stream's turn)
-          const bool seen = NQT == 2 && t == 1 && it < n_iter[0];
-          if (!seen && !full(t, fill)) { ok = false; break; }
-          // keys past the sequence's end have no weight, but what stands in their rows (stale or
-          // unwritten memory) may be NaN or infinite: zero those V rows before a product reads them
+      auto issue_pv = [&](int t, int it) -> bool {
+        const int fill = 2 * it + 1;
+        if (first_user(t, it)) {
+          if (!full(t, fill)) return false;
+          // Keys past the sequence's end have no weight, but what stands in their rows (stale or unwritten
+          // memory) may be NaN or infinite: zero those V rows before a product reads them.
           const int valid = seq.kv - (range.first + tile_of(t, it)) * 128;
-          if (valid < 128 && !seen) {
+          if (valid < 128) {
+            uint8_t* v_tile = sRing + stage(t, fill) * L::TILE;
             for (int i = lane; i < (128 - valid) * 8 * NB; i += 32) {
               const int c = i / ((128 - valid) * 8), in_box = i % ((128 - valid) * 8);
-              *reinterpret_cast<uint4*>(sRing + stage(t, fill) * L::TILE + c * L::BOX + valid * 128 + in_box * 16) =
-                  make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v_tile + c * L::BOX + valid * 128 + in_box * 16) = make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async_shared();
             __syncwarp();
           }
-          if (!wait(bar_p_lo + t, it & 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_pv(t, it, 0);
-          if (!wait(bar_p_hi + t, it & 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_pv(t, it, 1);
-          if (last_user(t, it)) mma_commit_warp(bar_empty + stage(t, fill));
-          if (it + 1 < n_iter[t]) {
-            if (!(NQT == 2 && t == 1 && it + 1 < n_iter[0]) && !full(t, fill + 1)) { ok = false; break; }
-            tc_fence_after();
-            issue_qk(t, it + 1);
+        }
+        if (!wait(bar_p_full + t, it & 1)) return false;
+        tc_fence_after();
+        const uint32_t v_base = ring + stage(t, fill) * L::TILE;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)  // 64 keys, 16 per product
+          mma_f16_ts_x4_warp<8, 16 * 128 / 16>(tmem + o_col(t), tmem + p_col(t) + half * 32,
+                                               make_smem_desc(v_base + half * 64 * 128, L::BOX, 1024, kSwizzle128B),
+                                               IDESC_PV, it == 0 && half == 0 ? 0u : 1u);
+        if (last_user(t, it)) mma_commit_warp(bar_empty + stage(t, fill));
+        if (L::OWN_P || it + 1 == n_iter[t]) mma_commit_warp(bar_pv + t);
+        return true;
+      };
+      bool ok = wait(bar_q, 0);
+      for (int t = 0; ok && t < 2; ++t)
+        if (n_iter[t] > 0) ok = issue_qk(t, 0);
+      for (int it = 0; ok && it < max(n_iter[0], n_iter[1]); ++it) {
+        for (int t = 0; ok && t < 2; ++t) {
+          if (it >= n_iter[t]) continue;
+          if constexpr (L::OWN_P) {
+            if (it + 1 < n_iter[t]) ok = issue_qk(t, it + 1);
+            ok = ok && issue_pv(t, it);
           } else {
-            mma_commit_warp(bar_o_done + t);
+            ok = issue_pv(t, it);
+            if (ok && it + 1 < n_iter[t]) ok = issue_qk(t, it + 1);
           }
         }
       }
@@ -344,6 +348,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_addr + s_col(t);
     const uint32_t tO = tmem + lane_addr + o_col(t);
+    const uint32_t tP = tmem + lane_addr + p_col(t);
     const int tok = tok0 + (NQT == 2 ? t * a.tile_tokens : 0) + r / a.G;
     const bool row_valid = r < a.tile_tokens * a.G && tok < seq.nq;
     const int lim = visible(a, seq, tok);  // this row's keys: [0, lim)
@@ -357,14 +362,22 @@ __global__ void __launch_bounds__(384, 1)
       if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full + t, it & 1, abort_flag))) { ok = false; break; }
       tc_fence_after();
       if (!warp_live) {  // no row of this warp exists: whatever stands in its lanes is never stored
-        mbar_arrive(bar_p_lo + t);
-        mbar_arrive(bar_p_hi + t);
+        if (L::OWN_P) {
+          // one arrival per tile: S of the next tile may come before the other warps' weights of this one
+          mbar_arrive(bar_s_free + t);
+          if (it > 0 && !__all_sync(0xffffffffu, mbar_wait(bar_pv + t, (it - 1) & 1, abort_flag))) { ok = false; break; }
+        }
+        mbar_arrive(bar_p_full + t);
         continue;
       }
       const int k0 = (range.first + tile_of(t, it)) * 128;
       uint32_t x[128];
       tmem_ld64_sync(tS + 0, *reinterpret_cast<uint32_t(*)[64]>(x + 0));
       tmem_ld64_sync(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(x + 64));
+      if (L::OWN_P) {
+        tc_fence_before();
+        mbar_arrive(bar_s_free + t);
+      }
       const bool masked = lim_warp < k0 + 128;
       if (masked) {
         const int seen = lim - k0;
@@ -383,9 +396,8 @@ __global__ void __launch_bounds__(384, 1)
         }
         return fmaxf(max3f(mx[0], mx[1], mx[2]), fmaxf(max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * a.scale_log2;
       };
-      // The offset moves when the maximum has passed it by 8 (also at the first finite maximum).  Every
-      // earlier product of the stream is complete then (they precede this S), and the next one waits for
-      // the arrivals below: O may be rescaled here.
+      // The offset moves when the maximum has passed it by 8 (also at the first finite maximum).  The next
+      // product waits for the arrival below, so O may be rescaled here once the last one is complete.
       auto move_offset = [&](float mx) {
         const bool move = mx > m_use + 8.f;
         const float alpha = move ? fast_exp2(m_use - mx) : 1.f;
@@ -401,8 +413,9 @@ __global__ void __launch_bounds__(384, 1)
           tmem_st32(tO + cb, ov);
         }
       };
-      // Weights of 64 keys into TMEM.  Masked weights are exactly 0 on the MUFU pipe (ex2(-inf)); the
-      // polynomial bottoms out at 2^-126 instead, so tiles with masked keys do not use it.
+      // Weights of 64 keys into TMEM, one pair in eight by the polynomial (the MUFU pipe alone would hold up
+      // the rest; more of it costs more issue slots than it saves).  Masked weights are exactly 0 on the MUFU
+      // pipe (ex2(-inf)); the polynomial bottoms out at 2^-126 instead, so tiles with masked keys do not use it.
       auto weights = [&](int half, auto poly, float2 (&sum)[4]) {
         const float off = kShift - (m_use == -INFINITY ? 0.f : m_use);
         const float2 sc2 = make_float2(a.scale_log2, a.scale_log2), off2 = make_float2(off, off);
@@ -414,27 +427,24 @@ __global__ void __launch_bounds__(384, 1)
             const int c = 64 * half + cb + i;
             const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, off2);
             float2 p;
-            if (decltype(poly)::value && ((i >> 1) & 3) == 3) p = exp2_poly2(u);
+            if (decltype(poly)::value && ((i >> 1) & 7) == 7) p = exp2_poly2(u);
             else p = make_float2(fast_exp2(u.x), fast_exp2(u.y));
             sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
             pk[i >> 1] = pack16<BF16>(p.x, p.y);
           }
-          tmem_st16(tS + 32 * half + (cb >> 1), pk);
+          tmem_st16(tP + 32 * half + (cb >> 1), pk);
         }
       };
-      auto publish = [&](int half) {
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(half == 0 ? bar_p_lo + t : bar_p_hi + t);
-      };
+      if (L::OWN_P && it > 0) {  // the product of the tile before has read its weights (else: it precedes this S)
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_pv + t, (it - 1) & 1, abort_flag))) { ok = false; break; }
+        tc_fence_after();
+      }
       if (it == 0 || masked) {
         const float mx = row_max();
         if (it == 0) m_use = mx;
         else if (__any_sync(0xffffffffu, mx > m_use + 8.f)) move_offset(mx);
         weights(0, std::false_type{}, lsum);
-        publish(0);
         weights(1, std::false_type{}, lsum);
-        publish(1);
       } else {
         // The offset hardly ever moves after the first tiles: the first 64 weights are taken at the old
         // one while the maximum is found beside them, and taken again if it did move.
@@ -450,16 +460,18 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) lsum[i] = sum[i];
         }
-        publish(0);
         weights(1, std::true_type{}, lsum);
-        publish(1);
       }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar_p_full + t);
     }
 
     // ---- epilogue
     const float2 l2 = __fadd2_rn(__fadd2_rn(lsum[0], lsum[1]), __fadd2_rn(lsum[2], lsum[3]));
     float l = l2.x + l2.y;
-    if (ok && n_iter[t] > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar_o_done + t, 0, abort_flag));
+    if (ok && n_iter[t] > 0)
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_pv + t, L::OWN_P ? (n_iter[t] - 1) & 1 : 0, abort_flag));
     tc_fence_after();
     float keep = 1.f, take = 0.f;  // factors of this stream's O and of stream 1's (NQT = 1)
     bool join = false;
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(384, 1)
       float4* sO = reinterpret_cast<float4*>(sRing);
       if (join) {
         if (t == 1) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_o_done, 0, abort_flag)) && ok;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_drain, 0, abort_flag)) && ok;
           if (ok && warp_live) {
             sML[r] = make_float2(m_use, l);
 #pragma unroll
