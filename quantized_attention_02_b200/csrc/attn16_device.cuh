@@ -36,6 +36,11 @@ __device__ __forceinline__ Sequence sequence(const Attn16Args& a, int b) {
   return s;
 }
 
+// Key tiles that `tokens` tokens from tok0 on see together: those of the last one.
+__device__ __forceinline__ int key_tiles(const Attn16Args& a, const Sequence& s, int tok0, int tokens) {
+  return (visible(a, s, min(s.nq, tok0 + tokens) - 1) + 127) / 128;
+}
+
 // Element offset of head h of the sequence's token `tok` in O.
 __device__ __forceinline__ long long out_offset(const Attn16Args& a, const Sequence& s, int tok, int h) {
   return (a.cu_q ? 0 : s.b * a.o_sb) + h * a.o_sh + static_cast<long long>(s.token0 + tok) * a.o_sn;

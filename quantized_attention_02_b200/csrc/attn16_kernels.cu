@@ -78,11 +78,6 @@ __device__ __forceinline__ KeyRange key_range(int nt, int splits, int min_chunk,
   return r;
 }
 
-// Key tiles the CTA's query tiles see together: those of the last token.
-__device__ __forceinline__ int key_tiles(const Attn16Args& a, const Sequence& s, int tok0, int cta_tokens) {
-  return (visible(a, s, min(s.nq, tok0 + cta_tokens) - 1) + 127) / 128;
-}
-
 template <int D, bool BF16, int NQT>
 __global__ void __launch_bounds__(384, 1)
     attn16_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

@@ -7,6 +7,13 @@
 
 namespace sage {
 
+// Where a CTA's share of the axis of key tiles begins, for the kernel that joins the parts: `off` tiles into an item
+// of `units` tiles that begins at `first` (off 0: with an item, or there is no share).
+struct CutNote {
+  long long first, share;
+  int b, token0, nq, tok0, hk, off, units;
+};
+
 struct Attn16Args {
   void* o;
   long long o_sb, o_sh, o_sn;   // element strides of O
@@ -21,8 +28,10 @@ struct Attn16Args {
   int splits, min_chunk;        // key axis: at most splits parts of at least min_chunk key tiles
   float* part_o;                // [token][head][splits][D] fp32, unnormalised (splits > 1)
   float2* part_ml;              // [token][head][splits] (row maximum in log2 units, row sum)
+  CutNote* cuts;                // [CTA], where the axis is cut into shares (a workspace too)
   float scale_log2;             // sm_scale * log2(e)
   bool causal;
+  bool cut;                     // pairs of tiles: cut the key axis into equal shares (attn_pair_kernels.cu)
 };
 
 // The tensor maps (16-bit, 128-byte swizzle, boxes of 64 channels):
@@ -37,6 +46,11 @@ struct Attn16Launch {
 };
 
 cudaError_t launch_attn16(const Attn16Launch& l, cudaStream_t st);
+
+// Many rows: pairs of query tiles, ctas CTAs; with a.cut part_o and part_ml hold pair_part_rows(ctas) rows.
+size_t pair_part_rows(int ctas);
+cudaError_t launch_attn_pair(const Attn16Launch& l, int ctas, cudaStream_t st);
+int read_and_clear_pair_error(cudaStream_t st, cudaError_t* err);
 
 // The same for few query rows (attn_step_kernels.cu): items of at most kStepRows rows, tile_tokens =
 // kStepRows / G tokens.  Of a, slots, splits and min_chunk are not used; part_o and part_ml hold

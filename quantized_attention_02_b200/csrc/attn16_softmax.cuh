@@ -1,0 +1,153 @@
+// attn16_softmax.cuh -- one 128-key tile of the online softmax with query rows on the TMEM lanes, shared by the
+// kernels of attn16_kernels.cu and attn_pair_kernels.cu.
+#pragma once
+#include <type_traits>
+
+#include "attn16_device.cuh"
+#include "attn_common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace sage {
+
+// d = 64 leaves TMEM columns for the weights beside the scores, so that the next scores can be computed as
+// soon as these are in registers; d = 128: the weights overwrite the scores
+template <int D>
+constexpr bool kOwnWeights = D == 64;
+
+// TMEM columns of stream t: scores, accumulator, 16-bit weights
+template <int D>
+struct Columns {
+  __host__ __device__ static constexpr uint32_t s(int t) { return 128u * t; }
+  __host__ __device__ static constexpr uint32_t o(int t) { return 256u + static_cast<uint32_t>(D) * t; }
+  __host__ __device__ static constexpr uint32_t p(int t) { return kOwnWeights<D> ? 384u + 64u * t : 128u * t; }
+};
+
+// A row's running offset (log2 units) and the sum of its weights.
+struct RowState {
+  float m_use;
+  float2 lsum[4];
+  __device__ __forceinline__ void clear() {
+    m_use = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lsum[i] = make_float2(0.f, 0.f);
+  }
+  __device__ __forceinline__ float sum() const {
+    const float2 l2 = __fadd2_rn(__fadd2_rn(lsum[0], lsum[1]), __fadd2_rn(lsum[2], lsum[3]));
+    return l2.x + l2.y;
+  }
+};
+
+// fp16 weights carry a factor 2^7, so that a row's small weights keep their bits (2^8 * 2^7 fits)
+template <bool BF16>
+constexpr float kWeightShift = BF16 ? 0.f : 7.f;
+
+// This thread's row of a score tile (TMEM column base tS) -> its weights (tP).  The row sees the tile's keys
+// below `seen`; `masked`: some row of the warp does not see all 128.  `fresh`: the row's first tile.
+// s_free (kOwnWeights): receives an arrival once the scores are in registers; prior: waits until the product
+// that read the last weights is done, false if that wait gave up.  On return the weights are stored but not
+// yet waited for (tcgen05.wait::st).
+template <int D, bool BF16, typename Prior>
+__device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_t tO, uint32_t tP, int seen, bool masked,
+                                             bool fresh, float scale_log2, uint64_t* s_free, Prior prior) {
+  uint32_t x[128];
+  tmem_ld64_sync(tS + 0, *reinterpret_cast<uint32_t(*)[64]>(x + 0));
+  tmem_ld64_sync(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(x + 64));
+  if constexpr (kOwnWeights<D>) {
+    tc_fence_before();
+    mbar_arrive(s_free);
+  }
+  if (masked) {
+#pragma unroll
+    for (int c = 0; c < 128; ++c) x[c] = c < seen ? x[c] : 0xFF800000u;
+  }
+  auto row_max = [&]() {  // log2 units
+    float mx[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[8 + k]));
+#pragma unroll
+    for (int c = 16; c < 128; c += 16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        mx[k] = max3f(mx[k], __uint_as_float(x[c + k]), __uint_as_float(x[c + 8 + k]));
+    }
+    return fmaxf(max3f(mx[0], mx[1], mx[2]), fmaxf(max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * scale_log2;
+  };
+  // The offset moves when the maximum has passed it by 8 (also at the first finite maximum).  The last
+  // product is complete, and the next one waits for this tile's weights: O may be rescaled here.
+  auto move_offset = [&](float mx) {
+    const bool move = mx > row.m_use + 8.f;
+    const float alpha = move ? fast_exp2(row.m_use - mx) : 1.f;
+    if (move) row.m_use = mx;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row.lsum[i] = __fmul2_rn(row.lsum[i], make_float2(alpha, alpha));
+#pragma unroll
+    for (int cb = 0; cb < D; cb += 32) {
+      uint32_t ov[32];
+      tmem_ld32_sync(tO + cb, ov);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+      tmem_st32(tO + cb, ov);
+    }
+  };
+  // Weights of 64 keys into TMEM, one pair in eight by the polynomial (the MUFU pipe alone would hold up
+  // the rest; more of it costs more issue slots than it saves).  Masked weights are exactly 0 on the MUFU
+  // pipe (ex2(-inf)); the polynomial bottoms out at 2^-126 instead, so tiles with masked keys do not use it.
+  auto weights = [&](int half, auto poly, float2 (&sum)[4]) {
+    const float off = kWeightShift<BF16> - (row.m_use == -INFINITY ? 0.f : row.m_use);
+    const float2 sc2 = make_float2(scale_log2, scale_log2), off2 = make_float2(off, off);
+#pragma unroll
+    for (int cb = 0; cb < 64; cb += 32) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const int c = 64 * half + cb + i;
+        const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, off2);
+        float2 p;
+        if (decltype(poly)::value && ((i >> 1) & 7) == 7) p = exp2_poly2(u);
+        else p = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+        sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
+        pk[i >> 1] = pack16<BF16>(p.x, p.y);
+      }
+      tmem_st16(tP + 32 * half + (cb >> 1), pk);
+    }
+  };
+  if (!prior()) return false;
+  if (fresh || masked) {
+    const float mx = row_max();
+    if (fresh) row.m_use = mx;
+    else if (__any_sync(0xffffffffu, mx > row.m_use + 8.f)) move_offset(mx);
+    weights(0, std::false_type{}, row.lsum);
+    weights(1, std::false_type{}, row.lsum);
+  } else {
+    // The offset hardly ever moves after the first tiles: the first 64 weights are taken at the old one
+    // while the maximum is found beside them, and taken again if it did move.
+    float2 sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = row.lsum[i];
+    weights(0, std::true_type{}, sum);
+    const float mx = row_max();
+    if (__any_sync(0xffffffffu, mx > row.m_use + 8.f)) {
+      move_offset(mx);
+      weights(0, std::true_type{}, row.lsum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) row.lsum[i] = sum[i];
+    }
+    weights(1, std::true_type{}, row.lsum);
+  }
+  return true;
+}
+
+// V rows [valid, 128) of a tile (boxes of 128 rows of 128 bytes) to zero, by one warp: keys past the
+// sequence's end have no weight, but what stands in their rows (stale or unwritten memory) may be NaN or
+// infinite, and the product would carry that on.
+template <int D>
+__device__ __forceinline__ void zero_v_tail(uint8_t* v_tile, int valid, int lane) {
+  const int pieces = (128 - valid) * 8;  // 16-byte pieces per box
+  for (int i = lane; i < pieces * (D / 64); i += 32)
+    *reinterpret_cast<uint4*>(v_tile + i / pieces * (128 * 128) + valid * 128 + i % pieces * 16) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_shared();
+  __syncwarp();
+}
+
+}  // namespace sage

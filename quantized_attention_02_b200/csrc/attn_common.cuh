@@ -66,6 +66,23 @@ __device__ __forceinline__ void reg_dealloc() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// The bounded wait of a role that runs ahead of the others (loads, bookkeeping): it sleeps between two looks,
+// so that it takes no issue slots from the warps that compute.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    __nanosleep(200);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      *abort = 1;
+      atomicExch(&g_device_error, kDevTimeoutBarrier);
+      return false;
+    }
+  }
+}
+
 // Bounded wait used on exit paths: ignores the abort flag, records a timeout.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();

@@ -40,7 +40,6 @@ namespace {
 constexpr int kUnit = 128;     // keys per unit: one tile
 constexpr int kWarps = 6;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kJoinWarps = 4;
 constexpr int kMinShare = 1;   // units per CTA at least
 constexpr int R = kStepRows;
 
@@ -203,7 +202,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   Walk walk;
   walk.u = blockIdx.x * share;
   walk.end = min(total, walk.u + share);
-  if (walk.u >= walk.end) return;
+  if (walk.u >= walk.end) {
+    if (threadIdx.x == 0 && a.cuts) a.cuts[blockIdx.x] = CutNote{};  // no cut
+    return;
+  }
   walk.b = 0;
   walk.prefix = 0;
   if (a.B > 1) {  // its first sequence: a scan over the sequences, kThreads at a time
@@ -267,6 +269,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     walk.prefix = found_prefix;
   }
   walk.it = items_of(s, walk.b);
+  if (threadIdx.x == 0 && a.cuts) {
+    const long long at = walk.u - walk.prefix;
+    const int item = static_cast<int>(at / walk.it.units), off = static_cast<int>(at % walk.it.units);
+    a.cuts[blockIdx.x] = CutNote{walk.u - off, share, walk.b, walk.it.seq.token0, walk.it.seq.nq,
+                                 item / a.Hk * s.tile_tokens, item % a.Hk, off, walk.it.units};
+  }
   Segment seg;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag));
@@ -560,60 +568,49 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Joins the items that a cut went through, in the order of their parts.  One CTA per (sequence, key head),
-// a warp per row.
+// Joins the items that a cut went through, in the order of their parts.  One CTA per cut between two shares, a
+// warp per row; an item that more than one cut goes through is joined by its first one.
+constexpr int kJoinThreads = 32 * R;
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__((32 * kJoinWarps)) attn_step_join_kernel(const __grid_constant__ StepArgs s, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) attn_step_join_kernel(const __grid_constant__ StepArgs s) {
   const Attn16Args& a = s.a;
-  __shared__ long long scratch[kJoinWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = static_cast<int>(blockIdx.x) / a.Hk, hk = static_cast<int>(blockIdx.x) % a.Hk;
-  long long all = 0, before = 0;
-  for (int i = threadIdx.x; i < a.B; i += (32 * kJoinWarps)) {
-    const long long len = length_of(items_of(s, i));
-    all += len;
-    if (i < b) before += len;
-  }
-  all = block_sum<kJoinWarps>(all, scratch);
-  before = block_sum<kJoinWarps>(before, scratch);
-  const long long share = share_of(all, ctas);
-  const Items it = items_of(s, b);
+  const int r = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
   cudaGridDependencySynchronize();  // the parts are written
-  for (int item = hk; item < it.items; item += a.Hk) {
-    const long long first = before + static_cast<long long>(item) * it.units;
-    const int c0 = static_cast<int>(first / share), c1 = static_cast<int>((first + it.units - 1) / share);
-    if (c0 == c1) continue;
-    const int tok0 = item / a.Hk * s.tile_tokens;
-    const int rows = min(s.tile_tokens, it.seq.nq - tok0) * a.G;
-    // in its first CTA the item is the last one (part 1) unless the CTA begins with it
-    auto part = [&](int c) { return 2 * c + (c == c0 && first % share != 0 ? 1 : 0); };
-    for (int r = warp; r < rows; r += kJoinWarps) {
-      float m = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[part(c) * R + r].x);
+  const CutNote cut = a.cuts[blockIdx.x + 1];
+  if (cut.off == 0) return;  // no such share, or it begins with an item
+  const int c0 = static_cast<int>(cut.first / cut.share), c1 = static_cast<int>((cut.first + cut.units - 1) / cut.share);
+  if (c0 != static_cast<int>(blockIdx.x)) return;
+  // in its first CTA the item is the last one (part 1) unless the CTA begins with it
+  const bool late = cut.first % cut.share != 0;
+  const int tok = cut.tok0 + r / a.G;
+  if (r >= s.tile_tokens * a.G || tok >= cut.nq) return;
+  auto part = [&](int c) { return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * R + r; };
+  float m = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[part(c)].x);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      const float base = m == -INFINITY ? 0.f : m;
-      constexpr int C = D / 32;  // channels per lane
-      float acc[C] = {}, l = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const float2 ml = a.part_ml[part(c) * R + r];
-        const float f = fast_exp2(ml.x - base);
-        l = fmaf(ml.y, f, l);
-        const float* src = a.part_o + (static_cast<long long>(part(c)) * R + r) * D + lane * C;
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float base = m == -INFINITY ? 0.f : m;
+  constexpr int C = D / 32;  // channels per lane
+  float acc[C] = {}, l = 0.f;
+#pragma unroll 8
+  for (int c = c0; c <= c1; ++c) {
+    const float2 ml = a.part_ml[part(c)];
+    const float f = fast_exp2(ml.x - base);
+    l = fmaf(ml.y, f, l);
+    const float* src = a.part_o + part(c) * D + lane * C;
 #pragma unroll
-        for (int e = 0; e < C; e += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(src + e);
-          acc[e] = fmaf(y.x, f, acc[e]);
-          acc[e + 1] = fmaf(y.y, f, acc[e + 1]);
-        }
-      }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      uint16_t* dst = static_cast<uint16_t*>(a.o) + out_offset(a, it.seq, tok0 + r / a.G, hk * a.G + r % a.G) + lane * C;
-#pragma unroll
-      for (int e = 0; e < C; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < C; e += 2) {
+      const float2 y = *reinterpret_cast<const float2*>(src + e);
+      acc[e] = fmaf(y.x, f, acc[e]);
+      acc[e + 1] = fmaf(y.y, f, acc[e + 1]);
     }
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint16_t* dst = static_cast<uint16_t*>(a.o) + lane * C +
+                  out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G);
+#pragma unroll
+  for (int e = 0; e < C; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 template <int D, bool BF16>
@@ -628,15 +625,15 @@ cudaError_t launch_step_t(const StepLaunch& l, int ctas, cudaStream_t st) {
   if (e != cudaSuccess || ctas == 1) return e;
   // launched early, while the attention drains: it waits on the device for the parts
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(s.a.B) * s.a.Hk);
-  cfg.blockDim = dim3((32 * kJoinWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas) - 1);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_step_join_kernel<D, BF16>, s, ctas);
+  return cudaLaunchKernelEx(&cfg, attn_step_join_kernel<D, BF16>, s);
 }
 
 }  // namespace

@@ -539,7 +539,9 @@ int sage_last_device_error(void* stream) {
   if (code16 < 0) return SAGE_ERR_CUDA;
   const int code_step = sage::read_and_clear_step_error(static_cast<cudaStream_t>(stream), &e);
   if (code_step < 0) return SAGE_ERR_CUDA;
-  return code ? code : code16 ? code16 : code_step;
+  const int code_pair = sage::read_and_clear_pair_error(static_cast<cudaStream_t>(stream), &e);
+  if (code_pair < 0) return SAGE_ERR_CUDA;
+  return code ? code : code16 ? code16 : code_step ? code_step : code_pair;
 }
 
 

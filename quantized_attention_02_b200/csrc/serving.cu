@@ -102,15 +102,16 @@ int sm_count() {
   return sms;
 }
 
-// fp32 parts of `rows` rows: O, then (m, l).  Stream-ordered, freed by part_free.
-int part_alloc(sage::Attn16Args& a, void** ws, int64_t rows, int d, cudaStream_t st) {
-  const size_t o_bytes = static_cast<size_t>(rows) * d * sizeof(float);
-  if (sage::workspace_alloc(ws, o_bytes + static_cast<size_t>(rows) * sizeof(float2), st) != cudaSuccess) {
+// fp32 parts of `rows` rows: O, then (m, l), then the notes of `ctas` shares.  Stream-ordered, freed by part_free.
+int part_alloc(sage::Attn16Args& a, void** ws, int64_t rows, int ctas, int d, cudaStream_t st) {
+  const size_t o_bytes = static_cast<size_t>(rows) * d * sizeof(float), ml_bytes = static_cast<size_t>(rows) * sizeof(float2);
+  if (sage::workspace_alloc(ws, o_bytes + ml_bytes + ctas * sizeof(sage::CutNote), st) != cudaSuccess) {
     cudaGetLastError();
     return SAGE_ERR_NOMEM;
   }
   a.part_o = static_cast<float*>(*ws);
   a.part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(*ws) + o_bytes);
+  a.cuts = reinterpret_cast<sage::CutNote*>(static_cast<uint8_t*>(*ws) + o_bytes + ml_bytes);
   return SAGE_OK;
 }
 int part_free(void* ws, int rc, cudaStream_t st) {
@@ -127,11 +128,29 @@ int run_step(const sage::Attn16Launch& t, cudaStream_t st) {
   const int ctas = sage::step_ctas(l.s, sms);
   void* ws = nullptr;
   int rc = SAGE_OK;
-  if (ctas > 1 && (rc = part_alloc(l.s.a, &ws, static_cast<int64_t>(sage::step_part_rows(ctas)), l.D, st))) return rc;
+  if (ctas > 1 && (rc = part_alloc(l.s.a, &ws, static_cast<int64_t>(sage::step_part_rows(ctas)), ctas, l.D, st))) return rc;
   return part_free(ws, cuda_status(sage::launch_attn_step(l, ctas, st)), st);
 }
 
-// Tiles of query rows.  Fewer CTAs than SMs: the key axis is split so that each SM has a part, of 512 keys
+// Pairs of query tiles: many items are dealt out whole, few have their key tiles cut into equal shares (of 512
+// keys at least).
+int run_pair(sage::Attn16Launch& l, cudaStream_t st) {
+  sage::Attn16Args& a = l.a;
+  const int sms = sm_count();
+  if (sms <= 0) return SAGE_ERR_CUDA;
+  const int64_t items = static_cast<int64_t>(a.slots) * a.Hk;
+  if (items >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
+  a.cut = items < 4ll * sms;
+  a.min_chunk = 4;
+  const int64_t units = items * std::max<int64_t>(1, (a.Nk + 127ll) / 128);
+  const int ctas = static_cast<int>(std::min<int64_t>(sms, a.cut ? (units + a.min_chunk - 1) / a.min_chunk : items));
+  void* ws = nullptr;
+  int rc = SAGE_OK;
+  if (a.cut && ctas > 1 && (rc = part_alloc(a, &ws, static_cast<int64_t>(sage::pair_part_rows(ctas)), ctas, l.D, st))) return rc;
+  return part_free(ws, cuda_status(sage::launch_attn_pair(l, ctas, st)), st);
+}
+
+// One tile of query rows per CTA.  Fewer CTAs than SMs: the key axis is split so that each SM has a part, of 512 keys
 // at least.  How many parts a sequence really has follows on the device from its length.
 int run_attn16(sage::Attn16Launch& l, int Hq, int64_t ctas, cudaStream_t st) {
   sage::Attn16Args& a = l.a;
@@ -145,7 +164,7 @@ int run_attn16(sage::Attn16Launch& l, int Hq, int64_t ctas, cudaStream_t st) {
   void* ws = nullptr;
   int rc = SAGE_OK;
   if (a.splits > 1 &&
-      (rc = part_alloc(a, &ws, static_cast<int64_t>(a.cu_q ? 1 : a.B) * a.Nq * Hq * a.splits, l.D, st)))
+      (rc = part_alloc(a, &ws, static_cast<int64_t>(a.cu_q ? 1 : a.B) * a.Nq * Hq * a.splits, 0, l.D, st)))
     return rc;
   return part_free(ws, cuda_status(sage::launch_attn16(l, st)), st);
 }
@@ -268,6 +287,7 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
   l.pair = static_cast<int64_t>(T) * G > static_cast<int64_t>(B) * kTileRows;
   const int cta_tokens = (l.pair ? 2 : 1) * a.tile_tokens;
   a.slots = T / cta_tokens + B;
+  if (l.pair) return run_pair(l, static_cast<cudaStream_t>(stream));
   const int64_t tiles = std::max(std::min(B, T), (T + cta_tokens - 1) / cta_tokens);
   return run_attn16(l, Hq, tiles * Hk, static_cast<cudaStream_t>(stream));
 }
@@ -311,6 +331,7 @@ int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const 
   const int64_t slots = static_cast<int64_t>(B) * ((Nq + cta_tokens - 1) / cta_tokens);
   if (slots >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
   a.slots = static_cast<int>(slots);
+  if (l.pair) return run_pair(l, static_cast<cudaStream_t>(stream));
   return run_attn16(l, Hq, slots * Hk, static_cast<cudaStream_t>(stream));
 }
 
