@@ -57,4 +57,37 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
+// One row's parts c0 .. c1 joined by a warp, in their order: acc[e] = sum_c 2^(m_c - m) O_c, l likewise, m the largest
+// m_c.  ml(c): (m, l) of part c; o(c): where this lane's C channels of its O stand.  The lanes take the parts'
+// factors first, 32 at a time, so that the loads of O follow each other without waiting.
+template <int C, typename ML, typename O>
+__device__ __forceinline__ void join_parts(float (&acc)[C], float& l, int c0, int c1, ML ml, O o) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, ml(c).x);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const float base = m == -INFINITY ? 0.f : m;
+  for (int first = c0; first <= c1; first += 32) {
+    const int n = min(32, c1 - first + 1);
+    const float2 mine = lane < n ? ml(first + lane) : make_float2(-INFINITY, 0.f);
+    const float w = exp2f(mine.x - base);
+    float part_l = mine.y * w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, off);
+    l += part_l;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float f = __shfl_sync(0xffffffffu, w, i);
+      const float* src = o(first + i);
+#pragma unroll
+      for (int e = 0; e < C; e += 2) {
+        const float2 y = *reinterpret_cast<const float2*>(src + e);
+        acc[e] = fmaf(y.x, f, acc[e]);
+        acc[e + 1] = fmaf(y.y, f, acc[e + 1]);
+      }
+    }
+  }
+}
+
 }  // namespace sage

@@ -684,8 +684,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the items that a cut went through: o = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s, in the order of the
 // parts.  Grid: the cuts between two shares x eighths of an item's rows, a warp per row; an item that more
 // than one cut goes through is joined by its first one.
-constexpr int kJoinThreads = 1024;
-constexpr int kJoinSplit = kRows / (kJoinThreads / 32);
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSplit = 8;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kJoinThreads) attn_pair_join_kernel(const __grid_constant__ Attn16Args a, int ctas) {
@@ -697,36 +697,22 @@ __global__ void __launch_bounds__(kJoinThreads) attn_pair_join_kernel(const __gr
   if (c0 != static_cast<int>(blockIdx.x)) return;
   // in its first CTA the item is the last one (part 1) unless the CTA begins with it
   const bool late = cut.first % cut.share != 0;
-  const int row = static_cast<int>(blockIdx.y) * (kJoinThreads / 32) + static_cast<int>(threadIdx.x >> 5);
-  const int t = row >> 7, r = row & 127;
-  const int tok = cut.tok0 + t * a.tile_tokens + r / a.G;
-  if (r >= a.tile_tokens * a.G || tok >= cut.nq) return;
   constexpr int PER = D / 32;  // channels per lane
-  auto place = [&](int c) { return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * kRows + row; };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[place(c)].x);
+  for (int i = static_cast<int>(threadIdx.x >> 5); i < kRows / kJoinSplit; i += kJoinThreads / 32) {
+    const int row = static_cast<int>(blockIdx.y) * (kRows / kJoinSplit) + i, t = row >> 7, r = row & 127;
+    const int tok = cut.tok0 + t * a.tile_tokens + r / a.G;
+    if (r >= a.tile_tokens * a.G || tok >= cut.nq) continue;
+    auto place = [&](int c) { return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * kRows + row; };
+    float acc[PER] = {}, l = 0.f;
+    join_parts<PER>(acc, l, c0, c1, [&](int c) { return a.part_ml[place(c)]; },
+                    [&](int c) { return a.part_o + place(c) * D + lane * PER; });
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint16_t* dst = static_cast<uint16_t*>(a.o) + lane * PER +
+                    out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G);
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  const float base = m == -INFINITY ? 0.f : m;
-  float acc[PER] = {}, l = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = a.part_ml[place(c)];
-    const float w = fast_exp2(ml.x - base);
-    l = fmaf(ml.y, w, l);
-    const float* src = a.part_o + place(c) * D + lane * PER;
-#pragma unroll
-    for (int e = 0; e < PER; e += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src + e);
-      acc[e] = fmaf(y.x, w, acc[e]);
-      acc[e + 1] = fmaf(y.y, w, acc[e + 1]);
-    }
+    for (int e = 0; e < PER; e += 2)
+      *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint16_t* dst = static_cast<uint16_t*>(a.o) + out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G) + lane * PER;
-#pragma unroll
-  for (int e = 0; e < PER; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 template <int D, bool BF16>

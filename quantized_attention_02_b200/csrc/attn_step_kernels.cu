@@ -92,22 +92,13 @@ __device__ __forceinline__ Items items_of(const StepArgs& s, int b) {
 }
 __device__ __forceinline__ long long length_of(const Items& r) { return static_cast<long long>(r.items) * r.units; }
 
-// Sum over the block (all threads get it); `scratch`: WARPS values.
-template <int WARPS>
-__device__ __forceinline__ long long block_sum(long long v, long long* scratch) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  long long sum = 0;
-#pragma unroll
-  for (int w = 0; w < WARPS; ++w) sum += scratch[w];
-  return sum;
+// a / b for a >= 0, b > 0; by the short division where it fits
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a >> 32 == 0 ? static_cast<unsigned>(a) / static_cast<unsigned>(b) : a / b;
 }
 
 __device__ __forceinline__ long long share_of(long long total, int ctas) {
-  const long long even = (total + ctas - 1) / ctas;
+  const long long even = quotient(total + ctas - 1, ctas);
   return even > kMinShare ? even : kMinShare;
 }
 
@@ -130,6 +121,13 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
 }
 
+// The largest of a warp's values, in every lane.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 // One item's part of a share: key tiles [first, last) of it.
 struct Segment {
   Sequence seq;
@@ -150,8 +148,8 @@ struct Walk {
       it = items_of(s, ++b);
     }
     const long long at = u - prefix;
-    const int item = static_cast<int>(at / it.units);
-    g.first = static_cast<int>(at % it.units);
+    const int item = static_cast<int>(quotient(at, it.units));
+    g.first = static_cast<int>(at - static_cast<long long>(item) * it.units);
     g.last = static_cast<int>(min(static_cast<long long>(it.units), g.first + (end - u)));
     g.whole = g.first == 0 && g.last == it.units;
     g.tok0 = item / s.a.Hk * s.tile_tokens;
@@ -194,26 +192,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- this CTA's share of the units
-  long long mine = 0;
-  for (int b = threadIdx.x; b < a.B; b += kThreads) mine += length_of(items_of(s, b));
-  const long long total = block_sum<kWarps>(mine, scratch);
-  const long long share = share_of(total, gridDim.x);
+  // ---- this CTA's share of the units, and the sequence in which it begins: a scan over the sequences' lengths,
+  // kThreads at a time (twice when there are more)
   Walk walk;
-  walk.u = blockIdx.x * share;
-  walk.end = min(total, walk.u + share);
-  if (walk.u >= walk.end) {
-    if (threadIdx.x == 0 && a.cuts) a.cuts[blockIdx.x] = CutNote{};  // no cut
-    return;
-  }
-  walk.b = 0;
-  walk.prefix = 0;
-  if (a.B > 1) {  // its first sequence: a scan over the sequences, kThreads at a time
-    long long before = 0;
-    for (int base = 0; base < a.B; base += kThreads) {
+  long long share = 0;
+  {
+    long long before = 0, len = 0, incl = 0;
+    auto scan = [&](int base) {  // incl: length up to this thread's sequence, before: of all so far
       const int b = base + static_cast<int>(threadIdx.x);
-      const long long len = b < a.B ? length_of(items_of(s, b)) : 0;
-      long long incl = len;
+      len = b < a.B ? length_of(items_of(s, b)) : 0;
+      incl = len;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
         const long long v = __shfl_up_sync(0xffffffffu, incl, off);
@@ -222,19 +210,30 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncthreads();
       if (lane == 31) scratch[warp] = incl;
       __syncthreads();
-      long long sum = before;
+      incl += before;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) incl += scratch[w];
-        sum += scratch[w];
+        const long long v = scratch[w];
+        if (w < warp) incl += v;
+        before += v;
       }
-      const long long first = before + incl - len;
-      if (walk.u >= first && walk.u < first + len) {
-        found_b = b;
-        found_prefix = first;
+    };
+    for (int base = 0; base < a.B; base += kThreads) scan(base);
+    const long long total = before;
+    share = share_of(total, gridDim.x);
+    walk.u = blockIdx.x * share;
+    walk.end = min(total, walk.u + share);
+    if (walk.u >= walk.end) {
+      if (threadIdx.x == 0 && a.cuts) a.cuts[blockIdx.x] = CutNote{};  // no cut
+      return;
+    }
+    if (a.B > kThreads) before = 0;
+    for (int base = 0; base < a.B; base += kThreads) {
+      if (a.B > kThreads) scan(base);
+      if (walk.u >= incl - len && walk.u < incl) {
+        found_b = base + static_cast<int>(threadIdx.x);
+        found_prefix = incl - len;
       }
-      before = sum;
-      if (before > walk.u) break;
     }
   }
 
@@ -264,14 +263,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   cta_sync();  // lane 0 of warp 0 initialised the barriers alone; found_b is written
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (a.B > 1) {
-    walk.b = found_b;
-    walk.prefix = found_prefix;
-  }
+  walk.b = found_b;
+  walk.prefix = found_prefix;
   walk.it = items_of(s, walk.b);
   if (threadIdx.x == 0 && a.cuts) {
     const long long at = walk.u - walk.prefix;
-    const int item = static_cast<int>(at / walk.it.units), off = static_cast<int>(at % walk.it.units);
+    const int item = static_cast<int>(quotient(at, walk.it.units));
+    const int off = static_cast<int>(at - static_cast<long long>(item) * walk.it.units);
     a.cuts[blockIdx.x] = CutNote{walk.u - off, share, walk.b, walk.it.seq.token0, walk.it.seq.nq,
                                  item / a.Hk * s.tile_tokens, item % a.Hk, off, walk.it.units};
   }
@@ -282,12 +280,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   if (warp == 5) {
     // ============================================================ TMA: Q of each item, K and V tiles (lane i:
-    // the tile's page i).  An item's Q is asked for behind its first K and V: its buffer is free only when
+    // the tile's page i).  A later item's Q is asked for behind its first K and V: its buffer is free only when
     // the item before it has used it, and the ring goes on meanwhile.
     const int page = 1 << a.page_shift;
     const int pages_per_tile = a.page_table && page < 128 ? 128 >> a.page_shift : 1;
     const int rows_per_copy = 128 / pages_per_tile;
-    int fill = 0, n = 0;
+    int fill = 0, n = 0, q_asked = 0;
     bool ok = true;
     while (ok && walk.next(s, seg)) {
       // (outer coordinate) of this lane's copy of key tile kt; pages past the sequence or outside the
@@ -300,7 +298,20 @@ __global__ void __launch_bounds__(kThreads, 2)
           p = __ldg(a.page_table + static_cast<long long>(seg.seq.b) * a.pages_per_seq + (key >> a.page_shift));
         return p < 0 || p >= a.num_pages ? a.num_pages : p;
       };
+      auto load_q = [&]() -> bool {
+        if (n > 0 && !wait(bar_q_free, (n - 1) & 1)) return false;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar_q_full, static_cast<uint32_t>(s.tile_tokens * a.G * NB * 128));
+          for (int c = 0; c < NB; ++c)
+            tma_load_5d(sQ + c * L::Q_BOX, &tm_q, bar_q_full, 64 * c, 0, seg.seq.token0 + seg.tok0, seg.hk,
+                        a.cu_q ? 0 : seg.seq.b);
+        }
+        __syncwarp();
+        q_asked = n + 1;
+        return true;
+      };
       int outer = seg.first < seg.last ? page_of(seg.first) : 0;
+      if (seg.first < seg.last && n == 0) load_q();
       for (int kt = seg.first; ok && kt < seg.last; ++kt) {
         const int next = kt + 1 < seg.last ? page_of(kt + 1) : 0;  // in flight during this tile's waits
         const int row = a.page_table ? (kt * 128) & (page - 1) : kt * 128;
@@ -322,25 +333,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           __syncwarp();
         }
         outer = next;
-        if (ok && kt == seg.first) {
-          if (n > 0 && !wait(bar_q_free, (n - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar_q_full, static_cast<uint32_t>(s.tile_tokens * a.G * NB * 128));
-            for (int c = 0; c < NB; ++c)
-              tma_load_5d(sQ + c * L::Q_BOX, &tm_q, bar_q_full, 64 * c, 0, seg.seq.token0 + seg.tok0, seg.hk,
-                          a.cu_q ? 0 : seg.seq.b);
-          }
-          __syncwarp();
-          ++n;
-        }
+        if (ok && kt == seg.first && n > 0) ok = load_q();
       }
+      if (seg.first < seg.last) ++n;
     }
     if (*abort_flag && lane == 0) {  // let copies in flight land before the CTA exits
       for (int f = max(0, fill - NS); f < fill; ++f) mbar_drain(bar_full + f % NS, (f / NS) & 1);
-      if (n > 0) mbar_drain(bar_q_full, (n - 1) & 1);
+      if (q_asked > 0) mbar_drain(bar_q_full, (q_asked - 1) & 1);
     }
   } else if (warp == 4) {
     // ============================================================ MMA issuer
@@ -353,12 +352,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto issue_qk = [&](int f, int buf) {
       const uint32_t k_base = ring + (f % NS) * L::TILE;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {  // 16 channels: 32 bytes inside a 128-byte swizzled row
-        const uint32_t off = (kk % 4) * 32;
-        mma_f16_ss_warp(tmem + R * buf, make_smem_desc(k_base + (kk / 4) * L::BOX + off, 16, 1024, kSwizzle128B),
-                        make_smem_desc(q_base + (kk / 4) * L::Q_BOX + off, 16, 1024, kSwizzle128B), IDESC_QK,
-                        kk > 0 ? 1u : 0u);
-      }
+      for (int c = 0; c < NB; ++c)  // 16 channels per product: 32 bytes inside a 128-byte swizzled row
+        mma_f16_ss_x4_warp<2, 2>(tmem + R * buf, make_smem_desc(k_base + c * L::BOX, 16, 1024, kSwizzle128B),
+                                 make_smem_desc(q_base + c * L::Q_BOX, 16, 1024, kSwizzle128B), IDESC_QK, c > 0 ? 1u : 0u);
       mma_commit_warp(bar_empty + f % NS);
       mma_commit_warp(bar_s_full + buf);
     };
@@ -397,10 +393,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!wait(bar_p_full, tile & 1)) { ok = false; break; }
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)  // 16 keys: 16 rows of 128 bytes of the V tile, 32 bytes of a weight row
-          mma_f16_ss_warp(tmem + 2 * R, make_smem_desc(ring + st * L::TILE + kk * 16 * 128, L::BOX, 1024, kSwizzle128B),
-                          make_smem_desc(p_base + (kk / 4) * L::P_ATOM + (kk % 4) * 32, 16, 1024, kSwizzle128B), IDESC_PV,
-                          kt == seg.first && kk == 0 ? 0u : 1u);
+        for (int half = 0; half < 2; ++half)  // 16 keys per product: 16 rows of the V tile, 32 bytes of a weight row
+          mma_f16_ss_x4_warp<16 * 128 / 16, 2>(tmem + 2 * R, make_smem_desc(ring + st * L::TILE + half * 64 * 128, L::BOX, 1024, kSwizzle128B),
+                                               make_smem_desc(p_base + half * L::P_ATOM, 16, 1024, kSwizzle128B), IDESC_PV,
+                                               kt == seg.first && half == 0 ? 0u : 1u);
         mma_commit_warp(bar_empty + st);
         mma_commit_warp(bar_pv);
       }
@@ -451,29 +447,35 @@ __global__ void __launch_bounds__(kThreads, 2)
             break;
           }
           // ---- new offsets: maxima over the tile's keys
-          float top[R];
+          // (rows in fours, without a branch per row, so that their loads and maxima overlap; rows past `rows`
+          // compute on whatever there is)
+          float4* red4 = reinterpret_cast<float4*>(sRed);  // [4 warps][rows / 4]
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            float v = x[r];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-            top[r] = v;
-          }
-          if (lane == 0) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) sRed[warp * R + r] = top[r];
+          for (int r = 0; r < R; r += 4) {
+            if (r < rows) {
+              const float4 v = make_float4(warp_max(x[r]), warp_max(x[r + 1]), warp_max(x[r + 2]), warp_max(x[r + 3]));
+              if (lane == 0) red4[(warp * R + r) / 4] = v;
+            }
           }
           group_sync();
           float f[R];
           bool moved = false;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float v = fmaxf(fmaxf(sRed[r], sRed[R + r]), fmaxf(sRed[2 * R + r], sRed[3 * R + r]));
-            const bool move = v > m[r] + 8.f;  // also the first finite maximum
-            f[r] = move ? fast_exp2(m[r] - v) : 1.f;
-            if (move) m[r] = v;
-            l[r] *= f[r];
-            moved |= move;
+          for (int r = 0; r < R; r += 4) {
+            f[r] = f[r + 1] = f[r + 2] = f[r + 3] = 1.f;
+            if (r < rows) {
+              const float4 v0 = red4[r / 4], v1 = red4[(R + r) / 4], v2 = red4[(2 * R + r) / 4], v3 = red4[(3 * R + r) / 4];
+              const float v[4] = {fmaxf(fmaxf(v0.x, v1.x), fmaxf(v2.x, v3.x)), fmaxf(fmaxf(v0.y, v1.y), fmaxf(v2.y, v3.y)),
+                                  fmaxf(fmaxf(v0.z, v1.z), fmaxf(v2.z, v3.z)), fmaxf(fmaxf(v0.w, v1.w), fmaxf(v2.w, v3.w))};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const bool move = v[k] > m[r + k] + 8.f;  // also the first finite maximum
+                f[r + k] = move ? fast_exp2(m[r + k] - v[k]) : 1.f;
+                m[r + k] = move ? v[k] : m[r + k];
+                l[r + k] *= f[r + k];
+                moved |= move;
+              }
+            }
           }
           group_sync();  // sRed is read
           if (moved && kt > seg.first) {  // the same in every thread
@@ -493,24 +495,30 @@ __global__ void __launch_bounds__(kThreads, 2)
         // ---- weights: hi and lo into the two atoms (the product of the tile before has read them)
         uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          if (r < rows) {
-            const float2 p = make_float2(fast_exp2(x[r] + (kShift - (m[r] == -INFINITY ? 0.f : m[r]))),
-                                         fast_exp2(x[r + 1] + (kShift - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]))));
-            l[r] += p.x;
-            l[r + 1] += p.y;
-            split16<BF16>(p, hi[r / 2], lo[r / 2]);
+        for (int g = 0; g < R; g += 4) {
+          if (g < rows) {
+#pragma unroll
+            for (int r = g; r < g + 4; r += 2) {
+              const float2 p = make_float2(fast_exp2(x[r] + (kShift - (m[r] == -INFINITY ? 0.f : m[r]))),
+                                           fast_exp2(x[r + 1] + (kShift - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]))));
+              l[r] += p.x;
+              l[r + 1] += p.y;
+              split16<BF16>(p, hi[r / 2], lo[r / 2]);
+            }
           }
         }
         if (tile > 0) ok = wait(bar_pv, (tile - 1) & 1) && ok;
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          if (r < rows) {
-            const uint32_t p0 = p_key + r * 128 + ((chunk ^ (r & 7)) << 4), p1 = p_key + (r + 1) * 128 + ((chunk ^ ((r + 1) & 7)) << 4);
-            st_shared_u16(p0, hi[r / 2]);
-            st_shared_u16(p1, hi[r / 2] >> 16);
-            st_shared_u16(p0 + R * 128, lo[r / 2]);
-            st_shared_u16(p1 + R * 128, lo[r / 2] >> 16);
+        for (int g = 0; g < R; g += 4) {
+          if (g < rows) {
+#pragma unroll
+            for (int r = g; r < g + 4; r += 2) {
+              const uint32_t p0 = p_key + r * 128 + ((chunk ^ (r & 7)) << 4), p1 = p_key + (r + 1) * 128 + ((chunk ^ ((r + 1) & 7)) << 4);
+              st_shared_u16(p0, hi[r / 2]);
+              st_shared_u16(p1, hi[r / 2] >> 16);
+              st_shared_u16(p0 + R * 128, lo[r / 2]);
+              st_shared_u16(p1 + R * 128, lo[r / 2] >> 16);
+            }
           }
         }
         fence_proxy_async_shared();
@@ -518,42 +526,64 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_arrive(bar_p_full);
       }
       if (stop) break;
-      // ---- row sums over the 128 keys' threads, output of the item or its part
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r < rows) {
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
-          if (lane == 0) sRed[warp * R + r] = l[r];
-        }
-      }
-      group_sync();
+      // ---- row sums over the 128 keys' threads (through the weights' memory, whose product is done), then the
+      // output of the item or its part
       const bool some = seg.first < seg.last;
       if (some) ok = wait(bar_pv, (tile - 1) & 1) && ok;
       tc_fence_after();
-      uint32_t o[2 * R];
-      if (some) tmem_ld32_sync(lanes + 2 * R, o);
-      const bool stored = ok && !*abort_flag;
-      uint16_t* obase = static_cast<uint16_t*>(a.o) + c;
-      int tok = seg.tok0, h = 0;
+      float* sums = reinterpret_cast<float*>(sP);  // [row][key]
+      static_assert(R * 128 * 4 <= 2 * L::P_ATOM, "a row's 128 partial sums fit the weights' memory");
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r < rows) {
-          const float sum = sRed[r] + sRed[R + r] + sRed[2 * R + r] + sRed[3 * R + r];
-          const float acc = some ? __uint_as_float(o[r]) + __uint_as_float(o[R + r]) : 0.f;
-          if (c < D && stored) {
-            if (seg.whole) {
-              const float y = sum > 0.f ? acc / sum : 0.f;
-              obase[out_offset(a, seg.seq, tok, seg.hk * a.G + h)] = static_cast<uint16_t>(pack16<BF16>(y, 0.f));
-            } else {
-              a.part_o[(static_cast<long long>(seg.part) * R + r) * D + c] = acc;
-              if (c == 0) a.part_ml[seg.part * R + r] = make_float2(m[r], sum);
-            }
-          }
-          if (++h == a.G) h = 0, ++tok;
+      for (int g = 0; g < R; g += 4) {
+        if (g < rows) {
+#pragma unroll
+          for (int r = g; r < g + 4; ++r) sums[r * 128 + c] = l[r];
         }
       }
-      group_sync();  // sRed is read; O^T too: the arrivals of the next item's weights order what follows
+      uint32_t o[2 * R];
+      if (some) {
+        tmem_ld32_sync(lanes + 2 * R, o);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 2 * R; ++r) o[r] = 0u;
+      }
+      group_sync();
+      for (int r = warp; r < rows; r += 4) {
+        const float4 y = *reinterpret_cast<const float4*>(sums + r * 128 + 4 * lane);
+        float v = (y.x + y.y) + (y.z + y.w);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if (lane == 0) sRed[r] = seg.whole ? (v > 0.f ? 1.f / v : 0.f) : v;
+      }
+      group_sync();
+      if (c < D && ok && !*abort_flag) {
+        uint16_t* dst = static_cast<uint16_t*>(a.o) + out_offset(a, seg.seq, seg.tok0, seg.hk * a.G) + c;
+        const long long next_token = a.o_sn - (a.G - 1) * a.o_sh;
+        float* part = a.part_o + static_cast<long long>(seg.part) * R * D + c;
+        int h = 0;
+#pragma unroll
+        for (int g = 0; g < R; g += 4) {
+          if (g < rows) {
+            const float4 y = *reinterpret_cast<const float4*>(sRed + g);
+            const float sum[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = g + k;
+              const float acc = __uint_as_float(o[r]) + __uint_as_float(o[R + r]);
+              if (seg.whole) {
+                if (r < rows) *dst = static_cast<uint16_t>(pack16<BF16>(acc * sum[k], 0.f));
+              } else if (r < rows) {
+                part[r * D] = acc;
+                if (c == 0) a.part_ml[seg.part * R + r] = make_float2(m[r], sum[k]);
+              }
+              const bool wrap = ++h == a.G;
+              dst += wrap ? next_token : a.o_sh;
+              h = wrap ? 0 : h;
+            }
+          }
+        }
+      }
+      group_sync();  // sRed and the sums are read; O^T too: the arrivals of the next item's weights order what follows
       tc_fence_before();
     }
   }
@@ -586,26 +616,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_step_join_kernel(const __gr
   const int tok = cut.tok0 + r / a.G;
   if (r >= s.tile_tokens * a.G || tok >= cut.nq) return;
   auto part = [&](int c) { return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * R + r; };
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, a.part_ml[part(c)].x);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  const float base = m == -INFINITY ? 0.f : m;
   constexpr int C = D / 32;  // channels per lane
   float acc[C] = {}, l = 0.f;
-#pragma unroll 8
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = a.part_ml[part(c)];
-    const float f = fast_exp2(ml.x - base);
-    l = fmaf(ml.y, f, l);
-    const float* src = a.part_o + part(c) * D + lane * C;
-#pragma unroll
-    for (int e = 0; e < C; e += 2) {
-      const float2 y = *reinterpret_cast<const float2*>(src + e);
-      acc[e] = fmaf(y.x, f, acc[e]);
-      acc[e + 1] = fmaf(y.y, f, acc[e + 1]);
-    }
-  }
+  join_parts<C>(acc, l, c0, c1, [&](int c) { return a.part_ml[part(c)]; },
+                                [&](int c) { return a.part_o + part(c) * D + lane * C; });
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint16_t* dst = static_cast<uint16_t*>(a.o) + lane * C +
                   out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G);
