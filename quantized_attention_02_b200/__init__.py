@@ -440,22 +440,19 @@ def sageattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = F
 _DTYPE_CODES = {torch.float16: SAGE_F16, torch.bfloat16: SAGE_BF16}
 
 
-def _data(t: torch.Tensor):
-    return t.data_ptr() or None
-
-
 def _same(name: str, t, like: torch.Tensor, dtype, shape=None) -> None:
     """t is a CUDA tensor on like's device, of this element type and (where given) shape."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
+    if t.dtype is dtype and t.get_device() == like.get_device() and (shape is None or t.shape == shape):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device (there is no CPU path)")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
 def _dense(name: str, t, like: torch.Tensor, dtype, shape=None):
@@ -465,17 +462,18 @@ def _dense(name: str, t, like: torch.Tensor, dtype, shape=None):
     _same(name, t, like, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return _data(t)
+    return t.data_ptr() or None
 
 
 def _view(name: str, t, like: torch.Tensor, shape, order):
     """(pointer, strides) of a view with the channels innermost; order: the dimensions that are batch
-    (or page; None: no such dimension), head and token."""
+    (or page; -1: no such dimension), head and token."""
     _same(name, t, like, like.dtype, shape)
     st = t.stride()
-    if t.shape[-1] > 1 and st[-1] != 1:
+    if st[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must have its last dimension contiguous")
-    return _data(t), SageStrides(*(0 if i is None else st[i] for i in order))
+    b, h, n = order
+    return t.data_ptr() or None, SageStrides(st[b] if b >= 0 else 0, st[h], st[n])
 
 
 def _activations(q, dims: int, what: str):
@@ -492,24 +490,36 @@ def _activations(q, dims: int, what: str):
 
 def _call(fn, where: str, device: torch.device, stream, *args) -> None:
     """fn(*args, stream) with `device` current; stream None: the device's current stream."""
-    handle = torch.cuda.current_stream(device).cuda_stream if stream is None else (
-        stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    if device.index == torch.cuda.current_device():
+    index = device.index
+    if stream is None:
+        handle = _raw_stream(index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == torch.cuda.current_device():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
             rc = fn(*args, handle)
-    _check(rc, where)
+    if rc != SAGE_OK:
+        raise SageError(rc, where)
 
 
-def _empty(shape, like: torch.Tensor, stream) -> torch.Tensor:
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same number without building a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _empty(like: torch.Tensor, stream) -> torch.Tensor:
     """A dense output for a launch on `stream`, allocated on that stream."""
     if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def _tables(cos, sin, q):
@@ -547,8 +557,8 @@ def qk_norm_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, e
     [B, H, N, d] tensors, the layout sageattn takes.  q and k may be any views with contiguous channels,
     such as the transposed slices of one projection's output; k may be None.  See sage_qk_norm_rope."""
     _activations(q, 4, "a [B, H, N, d] tensor")
-    q_out = _empty(q.shape, q, stream)
-    k_out = None if k is None else _empty(k.shape, q, stream)
+    q_out = _empty(q, stream)
+    k_out = None if k is None else _empty(k, stream)
     sage_qk_norm_rope(q, k, q_out, k_out, cos, sin, positions, q_weight, k_weight, eps, interleaved, stream)
     return q_out, k_out
 
@@ -567,7 +577,7 @@ def sage_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, cos, sin, positio
     dtype = _activations(q, 3, "a [T, H, d] tensor")
     T, Hq, d = q.shape
     Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
-    order = (None, 1, 0)
+    order = (-1, 1, 0)
     qp, qs = _view("q", q, q, None, order)
     kp, ks = _view("k", k, q, (T, Hk, d), order)
     vp, vs = _view("v", v, q, (T, Hk, d), order)
@@ -589,7 +599,7 @@ def qk_norm_rope_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, q
     """q [T, Hq, d] after the norm and rotation as a new dense tensor; the new tokens' keys (normed and
     rotated) and values go into the paged cache in the same pass.  See sage_qk_norm_rope_append."""
     _activations(q, 3, "a [T, H, d] tensor")
-    q_out = _empty(q.shape, q, stream)
+    q_out = _empty(q, stream)
     sage_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, cos, sin, positions, slots, q_weight, k_weight, eps,
                              interleaved, stream)
     return q_out
@@ -603,8 +613,8 @@ def sage_paged_attn(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal: bo
     dtype = _activations(q, 3, "a [T, H, d] tensor")
     T, Hq, d = q.shape
     Hk = k_cache.shape[2] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
-    qp, qs = _view("q", q, q, None, (None, 1, 0))
-    op, os_ = _view("o", o, q, q.shape, (None, 1, 0))
+    qp, qs = _view("q", q, q, None, (-1, 1, 0))
+    op, os_ = _view("o", o, q, q.shape, (-1, 1, 0))
     kp, ks = _cache("k_cache", k_cache, q, Hk, d)
     vp, vs = _cache("v_cache", v_cache, q, Hk, d)
     if v_cache.shape != k_cache.shape:
@@ -624,7 +634,7 @@ def sageattn_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, causal: bool =
     [T, Hq, d] tensor (rows outside every sequence are not written); sm_scale defaults to d^-1/2.
     See sage_paged_attn; the cache is filled by qk_norm_rope_append."""
     _activations(q, 3, "a [T, H, d] tensor")
-    o = _empty(q.shape, q, stream)
+    o = _empty(q, stream)
     sage_paged_attn(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal,
                     1.0 / math.sqrt(q.shape[-1]) if sm_scale is None else sm_scale, stream)
     return o
@@ -650,6 +660,6 @@ def sageattn_cross(q, k, v, key_len=None, sm_scale: float | None = None, stream=
     """O = softmax(Q K^T sm_scale) V of q [B, Hq, Nq, d] against states of another length k, v [B, Hk, Nk, d],
     fp16 or bf16, as a new dense tensor; sm_scale defaults to d^-1/2.  See sage_cross_attn."""
     _activations(q, 4, "a [B, H, N, d] tensor")
-    o = _empty(q.shape, q, stream)
+    o = _empty(q, stream)
     sage_cross_attn(q, k, v, o, key_len, 1.0 / math.sqrt(q.shape[-1]) if sm_scale is None else sm_scale, stream)
     return o

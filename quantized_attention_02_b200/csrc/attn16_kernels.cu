@@ -34,6 +34,7 @@
 #include "attn16_kernels.cuh"
 #include "attn_common.cuh"
 #include "sm100_ptx.cuh"
+#include "workspace.cuh"
 
 namespace sage {
 namespace {
@@ -629,9 +630,8 @@ template <int D, bool BF16, int NQT>
 cudaError_t launch_t(const Attn16Launch& l, cudaStream_t st) {
   using L = Layout16<D, NQT>;
   auto kern = attn16_kernel<D, BF16, NQT>;
-  // the attribute belongs to the current device; setting it again is harmless and costs well under a
-  // microsecond, so nothing is remembered per device
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared_memory(allowed, reinterpret_cast<const void*>(kern), L::SMEM);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(l.a.slots) * l.a.splits * l.a.Hk;
   kern<<<grid, L::THREADS, L::SMEM, st>>>(l.tm_q, l.tm_k, l.tm_v, l.a);

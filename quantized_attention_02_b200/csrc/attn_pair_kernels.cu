@@ -31,6 +31,7 @@
 #include "attn16_device.cuh"
 #include "attn16_kernels.cuh"
 #include "attn16_softmax.cuh"
+#include "workspace.cuh"
 
 namespace sage {
 namespace {
@@ -719,8 +720,8 @@ template <int D, bool BF16>
 cudaError_t launch_t(const Attn16Launch& l, int ctas, cudaStream_t st) {
   using L = PairLayout<D>;
   auto kern = attn_pair_kernel<D, BF16>;
-  // the attribute belongs to the current device; setting it again is harmless, so nothing is remembered
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared_memory(allowed, reinterpret_cast<const void*>(kern), L::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, L::SMEM, st>>>(l.tm_q, l.tm_k, l.tm_v, l.a);
   e = cudaGetLastError();

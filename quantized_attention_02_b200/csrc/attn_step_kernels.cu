@@ -33,6 +33,7 @@
 #include "attn16_kernels.cuh"
 #include "attn_common.cuh"
 #include "sm100_ptx.cuh"
+#include "workspace.cuh"
 
 namespace sage {
 namespace {
@@ -632,7 +633,8 @@ cudaError_t launch_step_t(const StepLaunch& l, int ctas, cudaStream_t st) {
   const StepArgs& s = l.s;
   using L = StepLayout<D>;
   auto kern = attn_step_kernel<D, BF16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared_memory(allowed, reinterpret_cast<const void*>(kern), L::SMEM);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kThreads, L::SMEM, st>>>(l.tm_q, l.tm_k, l.tm_v, s);
   e = cudaGetLastError();
