@@ -33,7 +33,7 @@ SOURCES = {
     "mma_rate.cu": [],
     "sparse_kernels.cu": [],
     "rope_kernels.cu": [],
-    "attn16_kernels.cu": [],
+    "attn_tile_kernels.cu": [],
     "attn_step_kernels.cu": [],
     "attn_pair_kernels.cu": [],
     "serving.cu": [],

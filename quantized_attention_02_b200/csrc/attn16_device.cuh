@@ -57,37 +57,67 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
-// One row's parts c0 .. c1 joined by a warp, in their order: acc[e] = sum_c 2^(m_c - m) O_c, l likewise, m the largest
-// m_c.  ml(c): (m, l) of part c; o(c): where this lane's C channels of its O stand.  The lanes take the parts'
-// factors first, 32 at a time, so that the loads of O follow each other without waiting.
-template <int C, typename ML, typename O>
-__device__ __forceinline__ void join_parts(float (&acc)[C], float& l, int c0, int c1, ML ml, O o) {
+// Parts c0 .. c1 of ROWS rows joined by a warp, in the parts' order: acc[k][e] = sum_c 2^(m_c - m) O_c of row k, l
+// likewise, m the largest m_c.  at(k, c): the place of part c of row k in ml and in o (rows of D = 32 C fp32).
+// The lanes take the parts' factors first, 32 at a time, so that the loads of O follow each other without
+// waiting.
+template <int ROWS, int C, typename At>
+__device__ __forceinline__ void join_parts(float (&acc)[ROWS][C], float (&l)[ROWS], int c0, int c1, const float2* ml,
+                                           const float* o, At at) {
   const int lane = threadIdx.x & 31;
-  float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, ml(c).x);
+  float m[ROWS];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  const float base = m == -INFINITY ? 0.f : m;
+  for (int k = 0; k < ROWS; ++k) {
+    m[k] = -INFINITY;
+    l[k] = 0.f;
+#pragma unroll
+    for (int e = 0; e < C; ++e) acc[k][e] = 0.f;
+  }
+  for (int c = c0 + lane; c <= c1; c += 32) {
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) m[k] = fmaxf(m[k], ml[at(k, c)].x);
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m[k] = fmaxf(m[k], __shfl_xor_sync(0xffffffffu, m[k], off));
+    if (m[k] == -INFINITY) m[k] = 0.f;
+  }
   for (int first = c0; first <= c1; first += 32) {
     const int n = min(32, c1 - first + 1);
-    const float2 mine = lane < n ? ml(first + lane) : make_float2(-INFINITY, 0.f);
-    const float w = exp2f(mine.x - base);
-    float part_l = mine.y * w;
+    float w[ROWS];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) part_l += __shfl_xor_sync(0xffffffffu, part_l, off);
-    l += part_l;
-#pragma unroll 8
+    for (int k = 0; k < ROWS; ++k) {
+      const float2 mine = lane < n ? ml[at(k, first + lane)] : make_float2(-INFINITY, 0.f);
+      w[k] = exp2f(mine.x - m[k]);
+      float part = mine.y * w[k];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
+      l[k] += part;
+    }
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
-      const float f = __shfl_sync(0xffffffffu, w, i);
-      const float* src = o(first + i);
 #pragma unroll
-      for (int e = 0; e < C; e += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src + e);
-        acc[e] = fmaf(y.x, f, acc[e]);
-        acc[e + 1] = fmaf(y.y, f, acc[e + 1]);
+      for (int k = 0; k < ROWS; ++k) {
+        const float f = __shfl_sync(0xffffffffu, w[k], i);
+        const float* src = o + at(k, first + i) * (32 * C) + lane * C;
+#pragma unroll
+        for (int e = 0; e < C; e += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(src + e);
+          acc[k][e] = fmaf(y.x, f, acc[k][e]);
+          acc[k][e + 1] = fmaf(y.y, f, acc[k][e + 1]);
+        }
       }
     }
   }
+}
+
+// A joined row into O: this lane's C channels from `dst` on.
+template <bool BF16, int C>
+__device__ __forceinline__ void store_joined(uint16_t* dst, const float (&acc)[C], float l) {
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int e = 0; e < C; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 }  // namespace sage

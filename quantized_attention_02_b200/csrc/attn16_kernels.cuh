@@ -1,5 +1,6 @@
 // attn16_kernels.cuh -- launchers of the 16-bit attention kernels behind the paged attention and the cross
-// attention: attn16_kernels.cu (tiles of query rows) and attn_step_kernels.cu (few rows).
+// attention, by the query rows of a sequence and key head: attn_step_kernels.cu (16 at most),
+// attn_tile_kernels.cu (one tile) and attn_pair_kernels.cu (more).
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -23,11 +24,11 @@ struct Attn16Args {
   int pages_per_seq, num_pages, page_shift;
   int B, Nq, Nk;                // paged: Nq = all tokens, Nk = pages_per_seq * page size
   int Hk, G;                    // key heads, query heads per key head
-  int tile_tokens;              // tokens of a 128-row query tile: 128 / G
-  int slots;                    // query tile slots of the grid
+  int tile_tokens;              // tokens of a query tile: its rows / G
+  int slots;                    // places for query tiles (or pairs of them), see tile_of_slot
   int splits, min_chunk;        // key axis: at most splits parts of at least min_chunk key tiles
-  float* part_o;                // [token][head][splits][D] fp32, unnormalised (splits > 1)
-  float2* part_ml;              // [token][head][splits] (row maximum in log2 units, row sum)
+  float* part_o;                // fp32, unnormalised: rows of D channels of the parts that are joined
+  float2* part_ml;              // their (row maximum in log2 units, row sum)
   CutNote* cuts;                // [CTA], where the axis is cut into shares (a workspace too)
   float scale_log2;             // sm_scale * log2(e)
   bool causal;
@@ -42,10 +43,13 @@ struct Attn16Launch {
   CUtensorMap tm_q, tm_k, tm_v;
   int D;
   bool bf16;
-  bool pair;  // two query tiles per CTA (else one, its key tiles taken by two streams)
+  bool pair;  // items of two query tiles (else tiles alone)
 };
 
-cudaError_t launch_attn16(const Attn16Launch& l, cudaStream_t st);
+// One tile of query rows per CTA (attn_tile_kernels.cu): slots, splits and min_chunk say how the grid is laid out;
+// with splits > 1 part_o and part_ml hold tile_part_rows rows.
+size_t tile_part_rows(const Attn16Args& a);
+cudaError_t launch_attn_tile(const Attn16Launch& l, cudaStream_t st);
 
 // Many rows: pairs of query tiles, ctas CTAs; with a.cut part_o and part_ml hold pair_part_rows(ctas) rows.
 size_t pair_part_rows(int ctas);
@@ -70,6 +74,6 @@ int step_ctas(const StepArgs& s, int sms);
 size_t step_part_rows(int ctas);
 cudaError_t launch_attn_step(const StepLaunch& l, int ctas, cudaStream_t st);
 int read_and_clear_step_error(cudaStream_t st, cudaError_t* err);
-int read_and_clear_attn16_error(cudaStream_t st, cudaError_t* err);
+int read_and_clear_tile_error(cudaStream_t st, cudaError_t* err);
 
 }  // namespace sage

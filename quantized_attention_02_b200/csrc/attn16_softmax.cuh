@@ -42,12 +42,13 @@ template <bool BF16>
 constexpr float kWeightShift = BF16 ? 0.f : 7.f;
 
 // This thread's row of a score tile (TMEM column base tS) -> its weights (tP).  The row sees the tile's keys
-// below `seen`; `masked`: some row of the warp does not see all 128.  `fresh`: the row's first tile.
+// below `seen`, the warp's rows that count see seen_warp of them at least (128 or more: no mask).  `fresh`: the
+// row's first tile.
 // s_free (kOwnWeights): receives an arrival once the scores are in registers; prior: waits until the product
 // that read the last weights is done, false if that wait gave up.  On return the weights are stored but not
 // yet waited for (tcgen05.wait::st).
 template <int D, bool BF16, typename Prior>
-__device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_t tO, uint32_t tP, int seen, bool masked,
+__device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_t tO, uint32_t tP, int seen, int seen_warp,
                                              bool fresh, float scale_log2, uint64_t* s_free, Prior prior) {
   uint32_t x[128];
   tmem_ld64_sync(tS + 0, *reinterpret_cast<uint32_t(*)[64]>(x + 0));
@@ -56,9 +57,13 @@ __device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_
     tc_fence_before();
     mbar_arrive(s_free);
   }
-  if (masked) {
+  const bool masked = seen_warp < 128;
 #pragma unroll
-    for (int c = 0; c < 128; ++c) x[c] = c < seen ? x[c] : 0xFF800000u;
+  for (int cb = 0; cb < 128; cb += 32) {
+    if (seen_warp < cb + 32) {
+#pragma unroll
+      for (int c = cb; c < cb + 32; ++c) x[c] = c < seen ? x[c] : 0xFF800000u;
+    }
   }
   auto row_max = [&]() {  // log2 units
     float mx[8];
@@ -143,9 +148,10 @@ __device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_
 // infinite, and the product would carry that on.
 template <int D>
 __device__ __forceinline__ void zero_v_tail(uint8_t* v_tile, int valid, int lane) {
-  const int pieces = (128 - valid) * 8;  // 16-byte pieces per box
-  for (int i = lane; i < pieces * (D / 64); i += 32)
-    *reinterpret_cast<uint4*>(v_tile + i / pieces * (128 * 128) + valid * 128 + i % pieces * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c)
+    for (int at = valid * 128 + lane * 16; at < 128 * 128; at += 512)
+      *reinterpret_cast<uint4*>(v_tile + c * (128 * 128) + at) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_shared();
   __syncwarp();
 }

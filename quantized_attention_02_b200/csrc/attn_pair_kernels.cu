@@ -46,15 +46,18 @@ template <int D>
 struct PairLayout {
   static constexpr int BOX = 128 * 128;      // 128 rows of 64 channels (128-byte rows)
   static constexpr int TILE = BOX * (D / 64);  // one Q, K or V tile
-  static constexpr int NS = D == 128 ? 5 : 12;  // ring stages
+  static constexpr int NS = D == 128 ? 5 : 8;   // ring stages
+  static constexpr int QB = D == 128 ? 1 : 2;   // Q buffers per stream: few keys leave no time to fetch one in between
+  static constexpr bool STAGED = D == 64;       // O leaves through shared memory (there is none left at d = 128)
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_RING = 2 * TILE;
-  static constexpr int OFF_BAR = OFF_RING + NS * TILE;
-  static constexpr int NUM_BARS = 2 * NS + 6 * 2 + 1 + 2 * kPosts;
+  static constexpr int OFF_RING = 2 * QB * TILE;
+  static constexpr int OFF_STAGE = OFF_RING + NS * TILE;  // 32 rows of 128 bytes for each softmax warp
+  static constexpr int OFF_BAR = OFF_STAGE + (STAGED ? 8 * 4096 : 0);
+  static constexpr int NUM_BARS = 2 * NS + 2 * 2 * QB + 4 * 2 + 1 + 2 * kPosts;
   static constexpr int OFF_POSTS = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_MISC = OFF_POSTS + kPosts * 64;
   static constexpr int SMEM = OFF_MISC + 16 + 1024;
-  static_assert(SMEM + 1024 <= 227 * 1024 + 1024, "shared memory budget");
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
   static_assert(SMEM > 114 * 1024, "one CTA per SM: each allocates all of TMEM");
 };
 
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Attn16Args a) {
   using L = PairLayout<D>;
   using C = Columns<D>;
-  constexpr int NS = L::NS, NB = D / 64;
+  constexpr int NS = L::NS, NB = D / 64, QB = L::QB;
   constexpr bool OWN_P = kOwnWeights<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -273,10 +276,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* bar_full = bars;
   uint64_t* bar_empty = bar_full + NS;
+  uint64_t* bar_q_full = bar_empty + NS;       // [2 streams][QB]
+  uint64_t* bar_q_free = bar_q_full + 2 * QB;  // [2 streams][QB] the segment's last scores are computed
   // [2], one per stream:
-  uint64_t* bar_q_full = bar_empty + NS;
-  uint64_t* bar_q_free = bar_q_full + 2;  // the segment's last scores are computed
-  uint64_t* bar_s_full = bar_q_free + 2;  // scores of a key tile (and every product before them) done
+  uint64_t* bar_s_full = bar_q_free + 2 * QB;  // scores of a key tile (and every product before them) done
   uint64_t* bar_s_free = bar_s_full + 2;  // scores in registers (OWN_P)
   uint64_t* bar_p_full = bar_s_free + 2;  // weights written
   uint64_t* bar_pv = bar_p_full + 2;      // second product done (OWN_P: each; else: the segment's last)
@@ -314,8 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_empty + i, 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar_q_full + t, 1);
-      mbar_init(bar_q_free + t, 1);
+      for (int i = 0; i < QB; ++i) {
+        mbar_init(bar_q_full + t * QB + i, 1);
+        mbar_init(bar_q_free + t * QB + i, 1);
+      }
       mbar_init(bar_s_full + t, 1);
       mbar_init(bar_s_free + t, 128);
       mbar_init(bar_p_full + t, 128);
@@ -413,14 +418,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (!ok || seg.n(t) == 0) continue;
-            if (nq[t] > 0 && !wait(bar_q_free + t, (nq[t] - 1) & 1)) {
+            const int buf = t * QB + nq[t] % QB;
+            if (nq[t] >= QB && !wait(bar_q_free + buf, (nq[t] / QB - 1) & 1)) {
               ok = false;
               continue;
             }
             if (lane == 0) {
-              mbar_arrive_expect_tx(bar_q_full + t, static_cast<uint32_t>(a.tile_tokens * a.G * NB * 128));
+              mbar_arrive_expect_tx(bar_q_full + buf, static_cast<uint32_t>(a.tile_tokens * a.G * NB * 128));
               for (int c = 0; c < NB; ++c)
-                tma_load_5d(sQ + t * L::TILE + c * L::BOX, &tm_q, bar_q_full + t, 64 * c, 0,
+                tma_load_5d(sQ + buf * L::TILE + c * L::BOX, &tm_q, bar_q_full + buf, 64 * c, 0,
                             seg.token0 + seg.tok0 + t * a.tile_tokens, seg.hk, a.cu_q ? 0 : seg.b);
             }
             __syncwarp();
@@ -432,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int f = max(0, fill - NS); f < fill; ++f) mbar_drain(bar_full + f % NS, (f / NS) & 1);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          if (nq[t] > 0) mbar_drain(bar_q_full + t, (nq[t] - 1) & 1);
+          for (int i = max(0, nq[t] - QB); i < nq[t]; ++i) mbar_drain(bar_q_full + t * QB + i % QB, (i / QB) & 1);
       }
     } else if (warp == 1) {
       // ============================================================ MMA issuer of both streams, in turn: the
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < NB; ++c)  // 16 channels per product: 32 bytes inside a 128-byte swizzled row
-          mma_f16_ss_x4_warp<2, 2>(tmem + C::s(t), make_smem_desc(q_base + t * L::TILE + c * L::BOX, 16, 1024, kSwizzle128B),
+          mma_f16_ss_x4_warp<2, 2>(tmem + C::s(t), make_smem_desc(q_base + (t * QB + (nq[t] - 1) % QB) * L::TILE + c * L::BOX, 16, 1024, kSwizzle128B),
                                    make_smem_desc(ring + (fill % NS) * L::TILE + c * L::BOX, 16, 1024, kSwizzle128B),
                                    IDESC_QK, c > 0 ? 1u : 0u);
         mma_commit_warp(bar_s_full + t);
@@ -489,12 +495,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_qk = [&](const Steps& g, int b, auto t, int it) -> bool {
         const int fill = b + 2 * it;
         if ((t == 0 || it >= g.n0) && !full(fill)) return false;
-        if (it == 0 && !wait(bar_q_full + t, nq[t]++ & 1)) return false;
+        if (it == 0) {
+          const int i = nq[t]++;
+          if (!wait(bar_q_full + t * QB + i % QB, (i / QB) & 1)) return false;
+        }
         if (OWN_P && scores[t] > 0 && !wait(bar_s_free + t, (scores[t] - 1) & 1)) return false;
         ++scores[t];
         mma_qk(t, fill);
         if (t == 1 || it >= g.n1) mma_commit_warp(bar_empty + fill % NS);
-        if (it + 1 == g.n(t)) mma_commit_warp(bar_q_free + t);
+        if (it + 1 == g.n(t)) mma_commit_warp(bar_q_free + t * QB + (nq[t] - 1) % QB);
         return true;
       };
       auto issue_pv = [&](const Steps& g, int b, auto t, int it) -> bool {
@@ -550,8 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               return true;
             };
             const bool has = it < seg.n(t);
-            if constexpr (OWN_P) return follow() && (!has || issue_pv(seg, base, t, it));
-            else return (!has || issue_pv(seg, base, t, it)) && follow();
+            // (the next segment's Q may be on its way still: the last product goes first)
+            if (OWN_P && !last) return follow() && (!has || issue_pv(seg, base, t, it));
+            return (!has || issue_pv(seg, base, t, it)) && follow();
           };
           ok = turn(s0) && turn(s1);
         }
@@ -583,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = quad * 32 + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_addr + C::s(t), tO = tmem + lane_addr + C::o(t), tP = tmem + lane_addr + C::p(t);
-    const int r_tok = t * a.tile_tokens + r / a.G;  // token of the row within an item
+    const int r_tok = t * a.tile_tokens + r / a.G, r_head = r % a.G;  // the row's token within an item, its head in the group
     int tiles = 0, done = 0;  // score tiles taken, segments with keys finished
     bool ok = true;
     for (int i = 0; ok && wait(bar_posted + i % kPosts, (i / kPosts) & 1); ++i) {
@@ -611,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(bar_s_full + t, tiles & 1)) { ok = false; break; }
           tc_fence_after();
           if (warp_live) {
-            ok = softmax_tile<D, BF16>(row, tS, tO, tP, lim - it * 128, lim_warp < it * 128 + 128, it == 0, a.scale_log2,
+            ok = softmax_tile<D, BF16>(row, tS, tO, tP, lim - it * 128, lim_warp - it * 128, it == 0, a.scale_log2,
                                        bar_s_free + t, prior);
             tmem_wait_st();
             tc_fence_before();
@@ -637,9 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_valid = r < a.tile_tokens * a.G && tok < sq.nq;
         const bool whole = seg->whole;
         const float scale = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-        uint16_t* orow = static_cast<uint16_t*>(a.o) + out_offset(a, sq, tok, seg->hk * a.G + r % a.G);
+        uint16_t* orow = static_cast<uint16_t*>(a.o) + out_offset(a, sq, tok, seg->hk * a.G + r_head);
         const long long part = static_cast<long long>(seg->part) * kRows + t * 128 + r;
         if (!whole && row_valid) a.part_ml[part] = make_float2(row.m_use, l);
+        uint8_t* stage = smem + L::OFF_STAGE + (warp - 4) * 4096;  // [32 rows][8 pieces], piece p of row i at p ^ (i & 7)
 #pragma unroll
         for (int cb = 0; cb < D; cb += 32) {
           uint32_t ov[32];
@@ -649,21 +660,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) ov[i] = 0u;
           }
-          if (row_valid) {
-            if (whole) {
-              uint32_t w[16];
+          if (whole) {
+            uint32_t w[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                w[i] = pack16<BF16>(__uint_as_float(ov[2 * i]) * scale, __uint_as_float(ov[2 * i + 1]) * scale);
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack16<BF16>(__uint_as_float(ov[2 * i]) * scale, __uint_as_float(ov[2 * i + 1]) * scale);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(orow + cb + 8 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            } else {
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              if constexpr (L::STAGED) *reinterpret_cast<uint4*>(stage + lane * 128 + (((cb / 8 + i) ^ (lane & 7)) << 4)) = v;
+              else if (row_valid) *reinterpret_cast<uint4*>(orow + cb + 8 * i) = v;
+            }
+          } else if (row_valid) {
+            {
               uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * D + cb);
 #pragma unroll
               for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
             }
           }
+        }
+        if (L::STAGED && whole) {
+          // four whole rows per instruction (a row per lane would be 32 lines each: 8 of them hold up the
+          // load-store unit for 256 cycles a warp)
+          __syncwarp();
+          const unsigned long long at = row_valid ? reinterpret_cast<unsigned long long>(orow) : 0ull;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 4 * i + (lane >> 3);
+            const unsigned long long dst = __shfl_sync(0xffffffffu, at, row);
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+            if (dst) reinterpret_cast<uint4*>(dst)[lane & 7] = v;
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();  // O is read: the arrivals of the next segment's weights order what follows
@@ -683,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the items that a cut went through: o = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s, in the order of the
-// parts.  Grid: the cuts between two shares x eighths of an item's rows, a warp per row; an item that more
+// parts.  Grid: the cuts between two shares x eighths of an item's rows, a warp for four rows; an item that more
 // than one cut goes through is joined by its first one.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSplit = 8;
@@ -699,20 +727,20 @@ __global__ void __launch_bounds__(kJoinThreads) attn_pair_join_kernel(const __gr
   // in its first CTA the item is the last one (part 1) unless the CTA begins with it
   const bool late = cut.first % cut.share != 0;
   constexpr int PER = D / 32;  // channels per lane
-  for (int i = static_cast<int>(threadIdx.x >> 5); i < kRows / kJoinSplit; i += kJoinThreads / 32) {
-    const int row = static_cast<int>(blockIdx.y) * (kRows / kJoinSplit) + i, t = row >> 7, r = row & 127;
-    const int tok = cut.tok0 + t * a.tile_tokens + r / a.G;
-    if (r >= a.tile_tokens * a.G || tok >= cut.nq) continue;
-    auto place = [&](int c) { return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * kRows + row; };
-    float acc[PER] = {}, l = 0.f;
-    join_parts<PER>(acc, l, c0, c1, [&](int c) { return a.part_ml[place(c)]; },
-                    [&](int c) { return a.part_o + place(c) * D + lane * PER; });
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t* dst = static_cast<uint16_t*>(a.o) + lane * PER +
-                    out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G);
+  const int first_row = static_cast<int>(blockIdx.y) * (kRows / kJoinSplit) + 4 * static_cast<int>(threadIdx.x >> 5);
+  static_assert(kRows / kJoinSplit == 4 * (kJoinThreads / 32), "four rows per warp");
+  float acc[4][PER], l[4];
+  join_parts(acc, l, c0, c1, a.part_ml, a.part_o, [&](int k, int c) {
+    return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * kRows + first_row + k;
+  });
 #pragma unroll
-    for (int e = 0; e < PER; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
+  for (int k = 0; k < 4; ++k) {  // (rows that do not exist joined whatever stands in their places)
+    const int row = first_row + k, t = row >> 7, r = row & 127;
+    const int tok = cut.tok0 + t * a.tile_tokens + r / a.G;
+    if (r < a.tile_tokens * a.G && tok < cut.nq)
+      store_joined<BF16>(static_cast<uint16_t*>(a.o) + lane * PER +
+                             out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G),
+                         acc[k], l[k]);
   }
 }
 

@@ -31,6 +31,7 @@
 
 #include "attn16_device.cuh"
 #include "attn16_kernels.cuh"
+#include "attn16_softmax.cuh"
 #include "attn_common.cuh"
 #include "sm100_ptx.cuh"
 #include "workspace.cuh"
@@ -383,13 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // memory) may be NaN or infinite: zero those V rows before the product reads them
         const int valid = seg.seq.kv - kt * 128;
         if (valid < 128) {
-          for (int i = lane; i < (128 - valid) * 8 * NB; i += 32) {
-            const int c = i / ((128 - valid) * 8), in_box = i % ((128 - valid) * 8);
-            *reinterpret_cast<uint4*>(sRing + st * L::TILE + c * L::BOX + valid * 128 + in_box * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_shared();
-          __syncwarp();
+          zero_v_tail<D>(sRing + st * L::TILE, valid, lane);
         }
         if (!wait(bar_p_full, tile & 1)) { ok = false; break; }
         tc_fence_after();
@@ -616,16 +611,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_step_join_kernel(const __gr
   const bool late = cut.first % cut.share != 0;
   const int tok = cut.tok0 + r / a.G;
   if (r >= s.tile_tokens * a.G || tok >= cut.nq) return;
-  auto part = [&](int c) { return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * R + r; };
   constexpr int C = D / 32;  // channels per lane
-  float acc[C] = {}, l = 0.f;
-  join_parts<C>(acc, l, c0, c1, [&](int c) { return a.part_ml[part(c)]; },
-                                [&](int c) { return a.part_o + part(c) * D + lane * C; });
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint16_t* dst = static_cast<uint16_t*>(a.o) + lane * C +
-                  out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G);
-#pragma unroll
-  for (int e = 0; e < C; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
+  float acc[1][C], l[1];
+  join_parts(acc, l, c0, c1, a.part_ml, a.part_o,
+             [&](int, int c) { return static_cast<long long>(2 * c + (c == c0 && late ? 1 : 0)) * R + r; });
+  store_joined<BF16>(static_cast<uint16_t*>(a.o) + lane * C +
+                         out_offset(a, Sequence{cut.b, cut.token0, cut.nq, 0}, tok, cut.hk * a.G + r % a.G),
+                     acc[0], l[0]);
 }
 
 template <int D, bool BF16>

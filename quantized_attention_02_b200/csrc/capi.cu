@@ -535,13 +535,13 @@ int sage_last_device_error(void* stream) {
   cudaError_t e;
   const int code = sage::read_and_clear_device_error(static_cast<cudaStream_t>(stream), &e);
   if (code < 0) return SAGE_ERR_CUDA;
-  const int code16 = sage::read_and_clear_attn16_error(static_cast<cudaStream_t>(stream), &e);
-  if (code16 < 0) return SAGE_ERR_CUDA;
+  const int code_tile = sage::read_and_clear_tile_error(static_cast<cudaStream_t>(stream), &e);
+  if (code_tile < 0) return SAGE_ERR_CUDA;
   const int code_step = sage::read_and_clear_step_error(static_cast<cudaStream_t>(stream), &e);
   if (code_step < 0) return SAGE_ERR_CUDA;
   const int code_pair = sage::read_and_clear_pair_error(static_cast<cudaStream_t>(stream), &e);
   if (code_pair < 0) return SAGE_ERR_CUDA;
-  return code ? code : code16 ? code16 : code_step ? code_step : code_pair;
+  return code ? code : code_tile ? code_tile : code_step ? code_step : code_pair;
 }
 
 

@@ -155,7 +155,7 @@ int run_pair(sage::Attn16Launch& l, cudaStream_t st) {
 
 // One tile of query rows per CTA.  Fewer CTAs than SMs: the key axis is split so that each SM has a part, of 512 keys
 // at least.  How many parts a sequence really has follows on the device from its length.
-int run_attn16(sage::Attn16Launch& l, int Hq, int64_t ctas, cudaStream_t st) {
+int run_tile(sage::Attn16Launch& l, int64_t ctas, cudaStream_t st) {
   sage::Attn16Args& a = l.a;
   const int sms = sm_count();
   if (sms <= 0) return SAGE_ERR_CUDA;
@@ -166,10 +166,8 @@ int run_attn16(sage::Attn16Launch& l, int Hq, int64_t ctas, cudaStream_t st) {
   if (static_cast<int64_t>(a.slots) * a.splits * a.Hk >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
   void* ws = nullptr;
   int rc = SAGE_OK;
-  if (a.splits > 1 &&
-      (rc = part_alloc(a, &ws, static_cast<int64_t>(a.cu_q ? 1 : a.B) * a.Nq * Hq * a.splits, 0, l.D, st)))
-    return rc;
-  return part_free(ws, cuda_status(sage::launch_attn16(l, st)), st);
+  if (a.splits > 1 && (rc = part_alloc(a, &ws, static_cast<int64_t>(sage::tile_part_rows(a)), 0, l.D, st))) return rc;
+  return part_free(ws, cuda_status(sage::launch_attn_tile(l, st)), st);
 }
 
 // Which kernel: by the rows (tokens x group) that a key head of an average sequence has.
@@ -292,7 +290,7 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
   a.slots = T / cta_tokens + B;
   if (l.pair) return run_pair(l, static_cast<cudaStream_t>(stream));
   const int64_t tiles = std::max(std::min(B, T), (T + cta_tokens - 1) / cta_tokens);
-  return run_attn16(l, Hq, tiles * Hk, static_cast<cudaStream_t>(stream));
+  return run_tile(l, tiles * Hk, static_cast<cudaStream_t>(stream));
 }
 
 int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const sage_strides* q_st,
@@ -335,7 +333,7 @@ int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const 
   if (slots >= (1ll << 31)) return SAGE_ERR_UNSUPPORTED;
   a.slots = static_cast<int>(slots);
   if (l.pair) return run_pair(l, static_cast<cudaStream_t>(stream));
-  return run_attn16(l, Hq, slots * Hk, static_cast<cudaStream_t>(stream));
+  return run_tile(l, slots * Hk, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
