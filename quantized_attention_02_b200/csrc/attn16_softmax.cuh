@@ -41,42 +41,46 @@ struct RowState {
 template <bool BF16>
 constexpr float kWeightShift = BF16 ? 0.f : 7.f;
 
+// Weights 2^(s * scale - offset) of 32 scores into TMEM at tP, one pair in POLY by the polynomial (0: none; the
+// MUFU pipe alone would hold up the rest, more of it costs more issue slots than it saves), and their sums.
+template <bool BF16, int POLY>
+__device__ __forceinline__ void weights32(const uint32_t* x, uint32_t tP, float scale_log2, float off, float2 (&sum)[4]) {
+  const float2 sc2 = make_float2(scale_log2, scale_log2), off2 = make_float2(off, off);
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, off2);
+    float2 p;
+    if (POLY > 0 && (i >> 1) % (POLY > 0 ? POLY : 1) == POLY - 1) p = exp2_poly2(u);
+    else p = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+    sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
+    pk[i >> 1] = pack16<BF16>(p.x, p.y);
+  }
+  tmem_st16(tP, pk);
+}
+
+// The largest of N scores.
+template <int N>
+__device__ __forceinline__ float scores_max(const uint32_t* x) {
+  float mx[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[8 + k]));
+#pragma unroll
+  for (int c = 16; c < N; c += 16) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) mx[k] = max3f(mx[k], __uint_as_float(x[c + k]), __uint_as_float(x[c + 8 + k]));
+  }
+  return fmaxf(max3f(mx[0], mx[1], mx[2]), fmaxf(max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+}
+
 // This thread's row of a score tile (TMEM column base tS) -> its weights (tP).  The row sees the tile's keys
-// below `seen`, the warp's rows that count see seen_warp of them at least (128 or more: no mask).  `fresh`: the
-// row's first tile.
-// s_free (kOwnWeights): receives an arrival once the scores are in registers; prior: waits until the product
-// that read the last weights is done, false if that wait gave up.  On return the weights are stored but not
-// yet waited for (tcgen05.wait::st).
+// below `seen`; the warp's rows that count see seen_warp of them at least and seen_most at most.  `fresh`: the
+// row's first tile.  s_free (kOwnWeights): receives an arrival once the scores are read for the last time; prior:
+// waits until the product that read the last weights is done, false if that wait gave up.  On return the
+// weights are stored but not yet waited for (tcgen05.wait::st).
 template <int D, bool BF16, typename Prior>
 __device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_t tO, uint32_t tP, int seen, int seen_warp,
-                                             bool fresh, float scale_log2, uint64_t* s_free, Prior prior) {
-  uint32_t x[128];
-  tmem_ld64_sync(tS + 0, *reinterpret_cast<uint32_t(*)[64]>(x + 0));
-  tmem_ld64_sync(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(x + 64));
-  if constexpr (kOwnWeights<D>) {
-    tc_fence_before();
-    mbar_arrive(s_free);
-  }
-  const bool masked = seen_warp < 128;
-#pragma unroll
-  for (int cb = 0; cb < 128; cb += 32) {
-    if (seen_warp < cb + 32) {
-#pragma unroll
-      for (int c = cb; c < cb + 32; ++c) x[c] = c < seen ? x[c] : 0xFF800000u;
-    }
-  }
-  auto row_max = [&]() {  // log2 units
-    float mx[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) mx[k] = fmaxf(__uint_as_float(x[k]), __uint_as_float(x[8 + k]));
-#pragma unroll
-    for (int c = 16; c < 128; c += 16) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mx[k] = max3f(mx[k], __uint_as_float(x[c + k]), __uint_as_float(x[c + 8 + k]));
-    }
-    return fmaxf(max3f(mx[0], mx[1], mx[2]), fmaxf(max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * scale_log2;
-  };
+                                             int seen_most, bool fresh, float scale_log2, uint64_t* s_free, Prior prior) {
   // The offset moves when the maximum has passed it by 8 (also at the first finite maximum).  The last
   // product is complete, and the next one waits for this tile's weights: O may be rescaled here.
   auto move_offset = [&](float mx) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_
     if (move) row.m_use = mx;
 #pragma unroll
     for (int i = 0; i < 4; ++i) row.lsum[i] = __fmul2_rn(row.lsum[i], make_float2(alpha, alpha));
-#pragma unroll
+#pragma unroll 1
     for (int cb = 0; cb < D; cb += 32) {
       uint32_t ov[32];
       tmem_ld32_sync(tO + cb, ov);
@@ -94,52 +98,79 @@ __device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_
       tmem_st32(tO + cb, ov);
     }
   };
-  // Weights of 64 keys into TMEM, one pair in eight by the polynomial (the MUFU pipe alone would hold up
-  // the rest; more of it costs more issue slots than it saves).  Masked weights are exactly 0 on the MUFU
-  // pipe (ex2(-inf)); the polynomial bottoms out at 2^-126 instead, so tiles with masked keys do not use it.
-  auto weights = [&](int half, auto poly, float2 (&sum)[4]) {
-    const float off = kWeightShift<BF16> - (row.m_use == -INFINITY ? 0.f : row.m_use);
-    const float2 sc2 = make_float2(scale_log2, scale_log2), off2 = make_float2(off, off);
+  auto offset = [&]() { return kWeightShift<BF16> - (row.m_use == -INFINITY ? 0.f : row.m_use); };
+  if (fresh || seen_warp < 128) {
+    // A first tile, whose maximum has to be known before its weights, or one with masked keys.  Rolled loops over 32
+    // keys that read the scores twice: beside the pass below this is little code, and where keys are few,
+    // so that every tile comes here, it is the instruction fetch that counts.  Masked weights are exactly 0 on
+    // the MUFU pipe (ex2(-inf)); the polynomial bottoms out at 2^-126 instead and is not used.
+    const int most = min(seen_most, 128);
+    auto scores = [&](int cb, uint32_t (&x)[32]) {
+      tmem_ld32_sync(tS + cb, x);
+      if (seen_warp < cb + 32) {
 #pragma unroll
-    for (int cb = 0; cb < 64; cb += 32) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const int c = 64 * half + cb + i;
-        const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), sc2, off2);
-        float2 p;
-        if (decltype(poly)::value && ((i >> 1) & 7) == 7) p = exp2_poly2(u);
-        else p = make_float2(fast_exp2(u.x), fast_exp2(u.y));
-        sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
-        pk[i >> 1] = pack16<BF16>(p.x, p.y);
+        for (int c = 0; c < 32; ++c) x[c] = cb + c < seen ? x[c] : 0xFF800000u;
       }
-      tmem_st16(tP + 32 * half + (cb >> 1), pk);
+    };
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int cb = 0; cb < most; cb += 32) {
+      uint32_t x[32];
+      scores(cb, x);
+      mx = fmaxf(mx, scores_max<32>(x));
     }
-  };
-  if (!prior()) return false;
-  if (fresh || masked) {
-    const float mx = row_max();
+    mx *= scale_log2;
+    if (!prior()) return false;
     if (fresh) row.m_use = mx;
     else if (__any_sync(0xffffffffu, mx > row.m_use + 8.f)) move_offset(mx);
-    weights(0, std::false_type{}, row.lsum);
-    weights(1, std::false_type{}, row.lsum);
-  } else {
-    // The offset hardly ever moves after the first tiles: the first 64 weights are taken at the old one
-    // while the maximum is found beside them, and taken again if it did move.
-    float2 sum[4];
+    const float off = offset();
+    // (d = 128: the weights of 32 keys overwrite scores of keys before them, which are read)
+#pragma unroll 1
+    for (int cb = 0; cb < 128; cb += 32) {
+      uint32_t x[32];
+      if (cb < most) {
+        scores(cb, x);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = 0xFF800000u;
+      }
+      if (kOwnWeights<D> && cb == 96) {
+        tc_fence_before();
+        mbar_arrive(s_free);
+      }
+      weights32<BF16, 0>(x, tP + (cb >> 1), scale_log2, off, row.lsum);
+    }
+    return true;
+  }
+  uint32_t x[128];
+  tmem_ld64_sync(tS + 0, *reinterpret_cast<uint32_t(*)[64]>(x + 0));
+  tmem_ld64_sync(tS + 64, *reinterpret_cast<uint32_t(*)[64]>(x + 64));
+  if constexpr (kOwnWeights<D>) {
+    tc_fence_before();
+    mbar_arrive(s_free);
+  }
+  if (!prior()) return false;
+  // The offset hardly ever moves after the first tiles: the first 64 weights are taken at the old one while the
+  // maximum is found beside them, and taken again if it did move.
+  float2 sum[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum[i] = row.lsum[i];
+  float off = offset();
+  weights32<BF16, 8>(x, tP, scale_log2, off, sum);
+  weights32<BF16, 8>(x + 32, tP + 16, scale_log2, off, sum);
+  const float mx = scores_max<128>(x) * scale_log2;
+  if (__any_sync(0xffffffffu, mx > row.m_use + 8.f)) {
+    move_offset(mx);
+    off = offset();
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum[i] = row.lsum[i];
-    weights(0, std::true_type{}, sum);
-    const float mx = row_max();
-    if (__any_sync(0xffffffffu, mx > row.m_use + 8.f)) {
-      move_offset(mx);
-      weights(0, std::true_type{}, row.lsum);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) row.lsum[i] = sum[i];
-    }
-    weights(1, std::true_type{}, row.lsum);
+    weights32<BF16, 0>(x, tP, scale_log2, off, sum);
+    weights32<BF16, 0>(x + 32, tP + 16, scale_log2, off, sum);
   }
+  weights32<BF16, 8>(x + 64, tP + 32, scale_log2, off, sum);
+  weights32<BF16, 8>(x + 96, tP + 48, scale_log2, off, sum);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) row.lsum[i] = sum[i];
   return true;
 }
 

@@ -611,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_live = __any_sync(0xffffffffu, row_valid);
         int lim = visible(a, sq, tok) - seg->first * 128;  // the row sees keys [0, lim) of the segment's
         const int lim_warp = __reduce_min_sync(0xffffffffu, row_valid ? lim : 0x7fffffff);
+        const int lim_most = __reduce_max_sync(0xffffffffu, row_valid ? lim : 0);
         auto prior = [&]() -> bool {  // (d = 128: the last product precedes these scores)
           if (!OWN_P || tiles == 0) return true;
           const bool w = wait(bar_pv + t, (tiles - 1) & 1);
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(bar_s_full + t, tiles & 1)) { ok = false; break; }
           tc_fence_after();
           if (warp_live) {
-            ok = softmax_tile<D, BF16>(row, tS, tO, tP, lim - it * 128, lim_warp - it * 128, it == 0, a.scale_log2,
+            ok = softmax_tile<D, BF16>(row, tS, tO, tP, lim - it * 128, lim_warp - it * 128, lim_most - it * 128, it == 0, a.scale_log2,
                                        bar_s_free + t, prior);
             tmem_wait_st();
             tc_fence_before();

@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool row_valid = r < a.tile_tokens * a.G && tok < seq.nq;
     const int lim = visible(a, seq, tok) - range.first * 128;  // the row sees keys [0, lim) of the CTA's
     const int lim_warp = __reduce_min_sync(0xffffffffu, row_valid ? lim : 0x7fffffff);
+    const int lim_most = __reduce_max_sync(0xffffffffu, row_valid ? lim : 0);
     const bool warp_live = __any_sync(0xffffffffu, row_valid);  // else what stands in its lanes is never stored
     RowState row;
     row.clear();
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int k0 = (2 * it + t) * 128;
       if (warp_live) {
-        ok = softmax_tile<D, BF16>(row, tS, tO, tP, lim - k0, lim_warp - k0, it == 0, a.scale_log2, bar_s_free + t, prior);
+        ok = softmax_tile<D, BF16>(row, tS, tO, tP, lim - k0, lim_warp - k0, lim_most - k0, it == 0, a.scale_log2, bar_s_free + t, prior);
         tmem_wait_st();
         tc_fence_before();
       } else if (OWN_P) {
