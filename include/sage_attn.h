@@ -404,7 +404,9 @@ int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* 
  * 128 times it.  Values of kv_len are taken into [0, pages_per_seq * page_size], of cu_q into [0, T];
  * a page outside the cache reads as zeros.  Cache rows past a sequence's end are never used, whatever
  * they hold.  When few tokens meet long caches the key axis is split over CTAs and joined (fp32
- * parts in a stream-ordered workspace), in a fixed order: the same call gives the same bits. */
+ * parts in a stream-ordered workspace), in a fixed order: the same call gives the same bits.  A table
+ * for more than 2^24 keys, or more than 2^24 sequences: SAGE_ERR_UNSUPPORTED.  A cu_q that is not
+ * ascending leaves unspecified rows of o, never an access outside the tensors. */
 int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, void* o, const sage_strides* q_st,
                     const sage_strides* k_cache_st, const sage_strides* v_cache_st, const sage_strides* o_st,
                     const int32_t* page_table, const int32_t* cu_q, const int32_t* kv_len, int B, int T, int Hq,
@@ -415,7 +417,7 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
  * keys j < key_len[b] (all Nk when key_len is NULL; values are taken into [0, Nk]).  No key: 0.
  * q, o: [B,Hq,Nq,d]; k, v: [B,Hk,Nk,d] (may be NULL when Nk = 0); query head h uses key head
  * h / (Hq/Hk); Hq as above.  Keys past key_len are never used, whatever they hold.  Nq = 1 is a
- * decoder's single token. */
+ * decoder's single token.  More than 2^24 keys: SAGE_ERR_UNSUPPORTED. */
 int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const sage_strides* q_st,
                     const sage_strides* k_st, const sage_strides* v_st, const sage_strides* o_st,
                     const int32_t* key_len, int B, int Hq, int Hk, int Nq, int Nk, int d, float sm_scale, int dtype,

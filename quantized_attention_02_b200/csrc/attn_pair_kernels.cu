@@ -113,7 +113,7 @@ __device__ __forceinline__ bool slot_pair(const Attn16Args& a, int slot, Sequenc
   if (upto == 0) return false;
   seq = sequence(a, upto - 1);
   p = slot - (seq.token0 / cta_tokens + seq.b);
-  return p < pairs_of(a, seq);
+  return p >= 0 && p < pairs_of(a, seq);  // (negative: cu_q is not ascending)
 }
 
 // A CTA's walk through its share.

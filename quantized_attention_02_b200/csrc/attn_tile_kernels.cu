@@ -81,7 +81,7 @@ __device__ __forceinline__ bool tile_of_slot(const Attn16Args& a, int slot, Sequ
     seq = sequence(a, slot / per_b);
     tok0 = slot % per_b * a.tile_tokens;
   }
-  return tok0 < seq.nq;
+  return tok0 >= 0 && tok0 < seq.nq;  // (negative: cu_q is not ascending)
 }
 
 template <int D, bool BF16>

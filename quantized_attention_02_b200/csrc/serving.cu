@@ -170,6 +170,9 @@ int run_tile(sage::Attn16Launch& l, int64_t ctas, cudaStream_t st) {
   return part_free(ws, cuda_status(sage::launch_attn_tile(l, st)), st);
 }
 
+// Keys of a sequence: no wait inside the kernels then comes near their limit.
+constexpr int64_t kMaxKeys = 1 << 24;
+
 // Which kernel: by the rows (tokens x group) that a key head of an average sequence has.
 bool few_rows(int64_t tokens, int64_t sequences, int G) {
   return G <= sage::kStepRows && tokens * G <= sequences * sage::kStepRows;
@@ -258,7 +261,7 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
       !view_ok(o, o_st, 1, Hq, T) || !view_ok(k_cache, k_cache_st, num_pages, Hk, page_size) ||
       !view_ok(v_cache, v_cache_st, num_pages, Hk, page_size))
     return SAGE_ERR_INVALID;
-  if (static_cast<int64_t>(pages_per_seq) * page_size >= (1ll << 31) ||
+  if (static_cast<int64_t>(pages_per_seq) * page_size > kMaxKeys || B > (1 << 24) ||
       static_cast<int64_t>(T) * Hq >= (1ll << 31) || !strides_fit(q_st) || !strides_fit(k_cache_st) ||
       !strides_fit(v_cache_st))
     return SAGE_ERR_UNSUPPORTED;
@@ -277,7 +280,7 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
   a.causal = causal != 0;
   l.D = d;
   l.bf16 = dtype == SAGE_BF16;
-  const bool step = few_rows(T, B, G) && static_cast<int64_t>(B) * Hk < (1ll << 31);
+  const bool step = few_rows(T, B, G);
   a.tile_tokens = (step ? sage::kStepRows : kTileRows) / G;
   if (!query_map(&l.tm_q, l.bf16, q, *q_st, 1, Hk, G, T, d, a.tile_tokens) ||
       !key_map(&l.tm_k, l.bf16, k_cache, *k_cache_st, num_pages, Hk, page_size, d, std::min(128, page_size)) ||
@@ -303,7 +306,7 @@ int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const 
   if (B == 0 || Nq == 0) return SAGE_OK;
   if (!view_ok(q, q_st, B, Hq, Nq) || !view_ok(o, o_st, B, Hq, Nq)) return SAGE_ERR_INVALID;
   if (Nk > 0 && (!view_ok(k, k_st, B, Hk, Nk) || !view_ok(v, v_st, B, Hk, Nk))) return SAGE_ERR_INVALID;
-  if (static_cast<int64_t>(B) * Nq * Hq >= (1ll << 31) || Nk > (1 << 30) || !strides_fit(q_st) ||
+  if (static_cast<int64_t>(B) * Nq * Hq >= (1ll << 31) || Nk > kMaxKeys || !strides_fit(q_st) ||
       (Nk > 0 && (!strides_fit(k_st) || !strides_fit(v_st))))
     return SAGE_ERR_UNSUPPORTED;
   const int G = Hq / Hk;
@@ -317,7 +320,7 @@ int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const 
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   l.D = d;
   l.bf16 = dtype == SAGE_BF16;
-  const bool step = few_rows(Nq, 1, G) && static_cast<int64_t>(B) * Hk < (1ll << 31);
+  const bool step = few_rows(Nq, 1, G);
   a.tile_tokens = (step ? sage::kStepRows : kTileRows) / G;
   if (!query_map(&l.tm_q, l.bf16, q, *q_st, B, Hk, G, Nq, d, a.tile_tokens)) return SAGE_ERR_CUDA;
   if (Nk > 0) {

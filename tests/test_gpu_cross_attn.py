@@ -45,6 +45,8 @@ def check(o, q, k, v, lengths, sm_scale):
     (3, 5, 1, 3, 1000, 128, [1000, 0, 17]),      # fifteen rows of five heads
     (300, 2, 1, 2, 70, 64, None),                # many short sequences
     (2, 32, 16, 700, 4100, 128, None),
+    (4, 40, 40, 1000, 226, 64, [226, 64, 128, 1]),  # more items than four per SM: dealt out whole
+    (4, 80, 40, 500, 333, 128, [333, 0, 77, 129]),
     (2, 128, 1, 3, 300, 64, [300, 17]),          # the widest group: one token per tile
     (1, 96, 1, 5, 700, 128, None),
 ])
@@ -103,9 +105,10 @@ def test_output_view_and_rows_around_it(sa):
     assert (buf[:, 0] == 7).all() and (buf[:, 151] == 7).all() and (buf[:, :, 0] == 7).all() and (buf[:, :, 5] == 7).all()
 
 
-def test_streams_and_graph(sa):
+@pytest.mark.parametrize("Nq", [1, 40, 300])  # the kernel for few rows, for one tile, for pairs of tiles
+def test_streams_and_graph(sa, Nq):
     g = torch.Generator().manual_seed(2)
-    q = torch.randn(1, 8, 1, 128, generator=g).half().cuda()
+    q = torch.randn(1, 8, Nq, 128, generator=g).half().cuda()
     k, v = torch.randn(2, 1, 8, 4000, 128, generator=g).half().cuda()
     want = sa.sageattn_cross(q, k, v)
     torch.cuda.synchronize()

@@ -88,6 +88,7 @@ SEQS = {
     "one_chunk_among_none": [(0, 100)] * 30 + [(29, 800)] + [(0, 5)] * 10,
     "idle": [(0, 100), (0, 0)],
     "many_steps": [(1, 1 + 53 * i % 900) for i in range(700)],
+    "many_chunks": [(64 - i % 5, 64 + 13 * i % 300) for i in range(300)],
     "many": [(1 + i % 3, 1 + 37 * i % 400) for i in range(500)],
 }
 
@@ -137,6 +138,25 @@ def test_bad_pages_read_as_zeros_and_lengths_are_clamped(sa):
     assert (run(sa, p, True, 0.125)[:2] == 0).all()
 
 
+@pytest.mark.parametrize("cu", [[0, 300, 100, 400], [400, 0, 0, 50], [-7, 90, 10 ** 6, 3]])
+@pytest.mark.parametrize("Hq,Hk", [(4, 4), (8, 2), (64, 1)])
+def test_cu_q_that_is_not_ascending_stays_inside(sa, cu, Hq, Hk):
+    p, *_ = problem([(100, 100), (200, 200), (100, 300)], Hq, Hk, 64, 32, torch.float16, tail=0)
+    p["cu_q"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    buf = torch.full((600, Hq, 64), 3.0, dtype=torch.float16, device="cuda")
+    o = buf[100:500]
+    sa.sage_paged_attn(p["q"], p["k_cache"], p["v_cache"], o, p["page_table"], p["cu_q"], p["kv_len"], True, 0.125)
+    torch.cuda.synchronize()
+    assert (buf[:100] == 3).all() and (buf[500:] == 3).all()
+
+
+def test_no_pages_at_all(sa):
+    p, *_ = problem([(1, 64), (3, 64)], 2, 1, 64, 16, torch.float16)
+    p["page_table"] = p["page_table"][:, :0].contiguous()
+    o = run(sa, p, True, 0.125)
+    assert (o[:4] == 0).all() and (o[4:] == 99).all()
+
+
 def test_strided_queries_and_output(sa):
     seqs = [(30, 200), (1, 90)]
     p, keys, values, cu = problem(seqs, 6, 2, 64, 32, torch.bfloat16)
@@ -150,8 +170,9 @@ def test_strided_queries_and_output(sa):
     assert (buf[:, 0] == 5).all() and (buf[:, 7] == 5).all()
 
 
-def test_same_bits_again_and_under_capture(sa):
-    seqs = [(1, 7000), (1, 3000), (4, 500)]
+@pytest.mark.parametrize("new", [1, 20, 200])  # the kernel for few rows, for one tile, for pairs of tiles
+def test_same_bits_again_and_under_capture(sa, new):
+    seqs = [(new, 7000), (1, 3000), (4, 500)]
     p, keys, values, cu = problem(seqs, 8, 2, 128, 64, torch.bfloat16)
     want = run(sa, p, True, 0.09)
     o = torch.zeros_like(want)
@@ -173,10 +194,10 @@ def test_same_bits_again_and_under_capture(sa):
     torch.cuda.synchronize()
     assert all(torch.equal(x[:cu[-1]], want[:cu[-1]]) for x in got)
     # lengths that changed between replays are seen
-    p["kv_len"][0] = 100
-    keys[0], values[0] = keys[0][:100], values[0][:100]
+    p["kv_len"][0] = 1000
+    keys[0], values[0] = keys[0][:1000], values[0][:1000]
     graphs[0].replay()
-    check(o, p, [(1, 100), (1, 3000), (4, 500)], keys, values, cu, True, 0.09)
+    check(o, p, [(new, 1000), (1, 3000), (4, 500)], keys, values, cu, True, 0.09)
 
 
 def test_offsets_past_32_bits(sa):

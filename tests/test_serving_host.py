@@ -125,7 +125,7 @@ ATTN_REFUSED = [
     (dict(kc=None), INVALID), (dict(vc=ODD), INVALID), (dict(table=None), INVALID), (dict(cu=None), INVALID),
     (dict(len=None), INVALID), (dict(T=-1), INVALID), (dict(pages=0), INVALID), (dict(width=-1), INVALID),
     (dict(page=8), UNSUPPORTED), (dict(page=100), UNSUPPORTED), (dict(page=512), UNSUPPORTED),
-    (dict(width=1 << 27), UNSUPPORTED), (dict(T=1 << 29), UNSUPPORTED),
+    (dict(width=(1 << 20) + 1), UNSUPPORTED), (dict(B=(1 << 24) + 1), UNSUPPORTED), (dict(T=1 << 29), UNSUPPORTED),
 ], ids=lambda v: str(v))
 def test_paged_attn_refuses(sa, kw, status):
     assert paged(sa, **kw) == status
@@ -133,7 +133,7 @@ def test_paged_attn_refuses(sa, kw, status):
 
 @pytest.mark.parametrize("kw,status", ATTN_REFUSED + [
     (dict(k=None), INVALID), (dict(v=ODD), INVALID), (dict(Nq=-1), INVALID), (dict(Nk=-1), INVALID),
-    (dict(Nq=1 << 29), UNSUPPORTED), (dict(Nk=(1 << 30) + 1), UNSUPPORTED),
+    (dict(Nq=1 << 29), UNSUPPORTED), (dict(Nk=(1 << 24) + 1), UNSUPPORTED),
 ], ids=lambda v: str(v))
 def test_cross_attn_refuses(sa, kw, status):
     assert cross(sa, **kw) == status
