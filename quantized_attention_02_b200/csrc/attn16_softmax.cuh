@@ -1,5 +1,5 @@
 // attn16_softmax.cuh -- one 128-key tile of the online softmax with query rows on the TMEM lanes, shared by the
-// kernels of attn16_kernels.cu and attn_pair_kernels.cu.
+// kernels of attn_tile_kernels.cu and attn_pair_kernels.cu.
 #pragma once
 #include <type_traits>
 

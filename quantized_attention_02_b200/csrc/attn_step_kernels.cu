@@ -1,7 +1,7 @@
 // attn_step_kernels.cu -- 16-bit attention of few query rows (single tokens, very short chunks) over many
 // keys: paged or strided keys, grouped heads.
 //
-// Mathematics: as attn16_kernels.cu (online softmax in log2 units), with each weight p = 2^(u - m) split into
+// Mathematics: as attn_pair_kernels.cu (online softmax in log2 units), with each weight p = 2^(u - m) split into
 // two 16-bit parts, p = hi + lo, and two products: the matrix instructions take 16-bit operands, they
 // are far from busy here, and the weights then carry about twice the operand type's bits.
 //
@@ -15,7 +15,8 @@
 //     the narrow side: S^T = K Q^T (N = 16) and O^T = V^T P^T (N = 32: the columns of hi, then of lo), so
 //     that a tile costs 16 short MMAs and a thread computes the few weights of one key.  With the rows on
 //     the lanes 112 of them would idle in the products and, worse, in the softmax: measured 125 us against
-//     XXX us for 131072 keys of 8 heads of 128 channels.
+//     100 us for a token of 32 heads over 131072 keys of 8 heads of 128 channels, both with the joining (86 us of it
+//     this kernel, 6.2 TB/s); 48 tokens over 5300 keys each on average take 165 us, 6.2 TB/s.
 //   - A row's offset is common to all lanes; it is taken from the first tile and moves only when a lane sees
 //     a score 8 above it (one vote per tile), so no tile but the first needs a maximum over lanes.
 //

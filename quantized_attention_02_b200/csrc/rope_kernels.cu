@@ -9,12 +9,13 @@
 // Bound: device memory (each element read once, written once: 4 bytes), if the instructions are kept down: at
 // 6.5 TB/s an SM has about 90 issue slots for the 16 bytes of a lane.
 // Layout: a row of d channels belongs to d/8 lanes, 8 channels (16 bytes) each, so a row is one coalesced
-// 16-byte access per lane and the sum of squares a shuffle over those lanes.  A block works on four heads of
-// one tensor for its tokens (all four loads first), so that what a lane needs besides -- weight and rotation,
+// 16-byte access per lane and the sum of squares a shuffle over those lanes.  A block works on eight heads of
+// one tensor for its tokens (all eight loads first), so that what a lane needs besides -- weight and rotation,
 // multiplied together once -- is the same for all of them: y = r (x cw + x' sw), x' the pair's other channel
 // (its neighbour, or, half split, from another lane: shuffled as 16-bit pairs), r the row's norm.
-// 2 x (48 + 48) heads of 64 channels, 16384 tokens, fp16: 140 us, 5.7 TB/s (224 us with the norm, the weights and both
-// pair layouts worked out per head: 213 instructions per 16 bytes).
+// 2 x (48 + 48) heads of 64 channels, 16384 tokens, fp16: 125 us, 6.4 TB/s (224 us with the norm, the weights and
+// both pair layouts worked out per head: 213 instructions per 16 bytes; 141 us with four heads and 256 threads,
+// 168 us with two heads).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -55,13 +56,13 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-constexpr int kRopeThreads = 256;
-constexpr int kHeads = 4;  // heads per thread
+constexpr int kRopeThreads = 128;
+constexpr int kHeads = 8;  // heads per thread
 
 __host__ __device__ constexpr int head_groups(int heads) { return (heads + kHeads - 1) / kHeads; }
 
 template <int D, bool BF16, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int LANES = D / 8;  // lanes per row
   constexpr int TOKENS = kRopeThreads / LANES;
   // ---- the block's tensor and heads, this thread's token and channels
