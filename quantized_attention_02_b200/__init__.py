@@ -440,62 +440,65 @@ def sageattn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = F
 _DTYPE_CODES = {torch.float16: SAGE_F16, torch.bfloat16: SAGE_BF16}
 
 
-def _same(name: str, t, like: torch.Tensor, dtype, shape=None) -> None:
-    """t is a CUDA tensor on like's device, of this element type and (where given) shape."""
+# The checks cost host time in every call of a decoding step: each question is asked once per tensor, in one comparison
+# for the tensors that are right, and _refuse finds out afterwards what is wrong with the others.
+def _refuse(name: str, t, like: torch.Tensor, dtype, shape) -> None:
+    """Raise for what keeps t from being a tensor of this element type and shape on like's device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
-    if t.dtype is dtype and t.get_device() == like.get_device() and (shape is None or t.shape == shape):
-        return
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device (there is no CPU path)")
     if t.device != like.device:
         raise ValueError(f"{name} is on {t.device}, not on {like.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _dense(name: str, t, like: torch.Tensor, dtype, shape=None):
-    """Pointer of a dense array (None stays None)."""
+def _dense(name: str, t, like: torch.Tensor, dev: int, dtype, shape):
+    """Pointer of a dense array (None stays None); dev: like's device."""
     if t is None:
         return None
-    _same(name, t, like, dtype, shape)
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(name, t, like, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr() or None
 
 
-def _view(name: str, t, like: torch.Tensor, shape, order):
-    """(pointer, strides) of a view with the channels innermost; order: the dimensions that are batch
-    (or page; -1: no such dimension), head and token."""
-    _same(name, t, like, like.dtype, shape)
+def _view(name: str, t, like: torch.Tensor, dev: int, dtype, shape, b: int, h: int, n: int):
+    """(pointer, strides) of a view with the channels innermost; b, h, n: the dimensions that are batch
+    (or page; -1: no such dimension), head and token; dev: like's device."""
+    if type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(name, t, like, dtype, shape)
     st = t.stride()
-    if st[-1] != 1 and t.shape[-1] > 1:
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have its last dimension contiguous")
-    b, h, n = order
     return t.data_ptr() or None, SageStrides(st[b] if b >= 0 else 0, st[h], st[n])
 
 
 def _activations(q, dims: int, what: str):
+    """Device, element type and its code of the queries, which the other tensors have to match."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("expected a torch tensor")
     if not q.is_cuda:
         raise ValueError("tensor must live on a CUDA device (there is no CPU path)")
     if q.dim() != dims:
         raise ValueError(f"expected {what}")
-    if q.dtype not in _DTYPE_CODES:
-        raise ValueError(f"expected float16 or bfloat16, not {q.dtype}")
-    return _DTYPE_CODES[q.dtype]
+    dtype = q.dtype
+    if dtype not in _DTYPE_CODES:
+        raise ValueError(f"expected float16 or bfloat16, not {dtype}")
+    return q.get_device(), dtype, _DTYPE_CODES[dtype]
 
 
-def _call(fn, where: str, device: torch.device, stream, *args) -> None:
+def _call(fn, where: str, device: int, stream, *args) -> None:
     """fn(*args, stream) with `device` current; stream None: the device's current stream."""
-    index = device.index
     if stream is None:
-        handle = _raw_stream(index)
+        handle = _raw_stream(device)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index == torch.cuda.current_device():
+    if device == torch.cuda.current_device():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -522,10 +525,13 @@ def _empty(like: torch.Tensor, stream) -> torch.Tensor:
         return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
-def _tables(cos, sin, q):
+def _tables(cos, sin, q, dev: int):
+    """Pointers, rows and channels of the tables."""
     if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
         raise ValueError("cos and sin must be [table_rows, rot_dim / 2] tensors")
-    return _dense("cos", cos, q, torch.float32), _dense("sin", sin, q, torch.float32, cos.shape)
+    shape = cos.shape
+    return (_dense("cos", cos, q, dev, torch.float32, shape), _dense("sin", sin, q, dev, torch.float32, shape),
+            shape[0], 2 * shape[1])
 
 
 def sage_qk_norm_rope(q, k, q_out, k_out, cos, sin, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -533,22 +539,22 @@ def sage_qk_norm_rope(q, k, q_out, k_out, cos, sin, positions=None, q_weight=Non
     """Norm of each head of q [B, Hq, N, d] and k [B, Hk, N, d] (k and k_out may be None) and the position
     rotation, into q_out and k_out: strided fp16 or bf16 views with contiguous channels.  positions: int32
     [N] or [B, N], rows of cos / sin [table_rows, rot_dim / 2] (fp32); None: token n has position n."""
-    dtype = _activations(q, 4, "a [B, H, N, d] tensor")
-    B, Hq, N, d = q.shape
-    qp, qs = _view("q", q, q, None, (0, 1, 2))
-    qop, qos = _view("q_out", q_out, q, q.shape, (0, 1, 2))
+    dev, dt, code = _activations(q, 4, "a [B, H, N, d] tensor")
+    B, Hq, N, d = shape = q.shape
+    qp, qs = _view("q", q, q, dev, dt, shape, 0, 1, 2)
+    qop, qos = _view("q_out", q_out, q, dev, dt, shape, 0, 1, 2)
     kp = kop = ks = kos = None
     Hk = 0
     if k is not None:
         Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-        kp, ks = _view("k", k, q, (B, Hk, N, d), (0, 1, 2))
-        kop, kos = _view("k_out", k_out, q, (B, Hk, N, d), (0, 1, 2))
-    cp, sp = _tables(cos, sin, q)
+        kp, ks = _view("k", k, q, dev, dt, (B, Hk, N, d), 0, 1, 2)
+        kop, kos = _view("k_out", k_out, q, dev, dt, (B, Hk, N, d), 0, 1, 2)
+    cp, sp, rows, rot = _tables(cos, sin, q, dev)
     per_batch = positions is not None and positions.dim() == 2
-    pp = _dense("positions", positions, q, torch.int32, (B, N) if per_batch else (N,))
-    _call(get_lib().sage_qk_norm_rope, "sage_qk_norm_rope", q.device, stream, qp, kp, qop, kop, qs, ks, qos, kos,
-          _dense("q_weight", q_weight, q, q.dtype, (d,)), _dense("k_weight", k_weight, q, q.dtype, (d,)), cp, sp, pp,
-          int(per_batch), B, Hq, Hk, N, d, 2 * cos.shape[1], cos.shape[0], int(bool(interleaved)), float(eps), dtype)
+    pp = _dense("positions", positions, q, dev, torch.int32, (B, N) if per_batch else (N,))
+    _call(get_lib().sage_qk_norm_rope, "sage_qk_norm_rope", dev, stream, qp, kp, qop, kop, qs, ks, qos, kos,
+          _dense("q_weight", q_weight, q, dev, dt, (d,)), _dense("k_weight", k_weight, q, dev, dt, (d,)), cp, sp, pp,
+          int(per_batch), B, Hq, Hk, N, d, rot, rows, int(bool(interleaved)), float(eps), code)
 
 
 def qk_norm_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -563,10 +569,16 @@ def qk_norm_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, e
     return q_out, k_out
 
 
-def _cache(name: str, cache, q, Hk: int, d: int):
-    if not isinstance(cache, torch.Tensor) or cache.dim() != 4:
-        raise ValueError(f"{name} must be a [pages, page_size, Hk, d] tensor")
-    return _view(name, cache, q, (cache.shape[0], cache.shape[1], Hk, d), (0, 2, 1))
+def _caches(k_cache, v_cache, q, dev: int, dt, d: int):
+    """Views of both caches, then pages, page size and key heads."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a [pages, page_size, Hk, d] tensor")
+    if not isinstance(v_cache, torch.Tensor) or v_cache.dim() != 4:
+        raise ValueError("v_cache must be a [pages, page_size, Hk, d] tensor")
+    pages, size, Hk, _ = k_cache.shape
+    shape = (pages, size, Hk, d)
+    return (_view("k_cache", k_cache, q, dev, dt, shape, 0, 2, 1), _view("v_cache", v_cache, q, dev, dt, shape, 0, 2, 1),
+            pages, size, Hk)
 
 
 def sage_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, cos, sin, positions, slots, q_weight=None,
@@ -574,24 +586,19 @@ def sage_qk_norm_rope_append(q, k, v, q_out, k_cache, v_cache, cos, sin, positio
     """sage_qk_norm_rope for the new tokens q [T, Hq, d], k and v [T, Hk, d] of a serving step: the keys and
     v go to rows `slots` (int32 [T]; slot = page * page_size + row, outside the cache: not written) of
     k_cache and v_cache [pages, page_size, Hk, d] (strided views; page_size 16 .. 256, a power of two)."""
-    dtype = _activations(q, 3, "a [T, H, d] tensor")
-    T, Hq, d = q.shape
-    Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
-    order = (-1, 1, 0)
-    qp, qs = _view("q", q, q, None, order)
-    kp, ks = _view("k", k, q, (T, Hk, d), order)
-    vp, vs = _view("v", v, q, (T, Hk, d), order)
-    qop, qos = _view("q_out", q_out, q, q.shape, order)
-    kcp, kcs = _cache("k_cache", k_cache, q, Hk, d)
-    vcp, vcs = _cache("v_cache", v_cache, q, Hk, d)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    cp, sp = _tables(cos, sin, q)
-    _call(get_lib().sage_qk_norm_rope_append, "sage_qk_norm_rope_append", q.device, stream, qp, kp, vp, qop, kcp, vcp,
-          qs, ks, vs, qos, kcs, vcs, _dense("q_weight", q_weight, q, q.dtype, (d,)),
-          _dense("k_weight", k_weight, q, q.dtype, (d,)), cp, sp, _dense("positions", positions, q, torch.int32, (T,)),
-          _dense("slots", slots, q, torch.int32, (T,)), T, Hq, Hk, d, 2 * cos.shape[1], cos.shape[0],
-          k_cache.shape[0], k_cache.shape[1], int(bool(interleaved)), float(eps), dtype)
+    dev, dt, code = _activations(q, 3, "a [T, H, d] tensor")
+    T, Hq, d = shape = q.shape
+    (kcp, kcs), (vcp, vcs), pages, size, Hk = _caches(k_cache, v_cache, q, dev, dt, d)
+    qp, qs = _view("q", q, q, dev, dt, shape, -1, 1, 0)
+    kp, ks = _view("k", k, q, dev, dt, (T, Hk, d), -1, 1, 0)
+    vp, vs = _view("v", v, q, dev, dt, (T, Hk, d), -1, 1, 0)
+    qop, qos = _view("q_out", q_out, q, dev, dt, shape, -1, 1, 0)
+    cp, sp, rows, rot = _tables(cos, sin, q, dev)
+    _call(get_lib().sage_qk_norm_rope_append, "sage_qk_norm_rope_append", dev, stream, qp, kp, vp, qop, kcp, vcp, qs,
+          ks, vs, qos, kcs, vcs, _dense("q_weight", q_weight, q, dev, dt, (d,)),
+          _dense("k_weight", k_weight, q, dev, dt, (d,)), cp, sp,
+          _dense("positions", positions, q, dev, torch.int32, (T,)), _dense("slots", slots, q, dev, torch.int32, (T,)),
+          T, Hq, Hk, d, rot, rows, pages, size, int(bool(interleaved)), float(eps), code)
 
 
 def qk_norm_rope_append(q, k, v, cos, sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
@@ -610,22 +617,18 @@ def sage_paged_attn(q, k_cache, v_cache, o, page_table, cu_q, kv_len, causal: bo
     """Attention of the new tokens q [T, Hq, d] over a paged cache k_cache, v_cache [pages, page_size, Hk, d]
     into o [T, Hq, d]: sequence b has rows cu_q[b] .. cu_q[b+1] of q and kv_len[b] keys in the pages of
     page_table[b].  page_table int32 [B, pages_per_seq], cu_q int32 [B + 1], kv_len int32 [B]."""
-    dtype = _activations(q, 3, "a [T, H, d] tensor")
-    T, Hq, d = q.shape
-    Hk = k_cache.shape[2] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
-    qp, qs = _view("q", q, q, None, (-1, 1, 0))
-    op, os_ = _view("o", o, q, q.shape, (-1, 1, 0))
-    kp, ks = _cache("k_cache", k_cache, q, Hk, d)
-    vp, vs = _cache("v_cache", v_cache, q, Hk, d)
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
+    dev, dt, code = _activations(q, 3, "a [T, H, d] tensor")
+    T, Hq, d = shape = q.shape
+    (kp, ks), (vp, vs), pages, size, Hk = _caches(k_cache, v_cache, q, dev, dt, d)
+    qp, qs = _view("q", q, q, dev, dt, shape, -1, 1, 0)
+    op, os_ = _view("o", o, q, dev, dt, shape, -1, 1, 0)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [B, pages_per_seq] tensor")
-    B, width = page_table.shape
-    _call(get_lib().sage_paged_attn, "sage_paged_attn", q.device, stream, qp, kp, vp, op, qs, ks, vs, os_,
-          _dense("page_table", page_table, q, torch.int32), _dense("cu_q", cu_q, q, torch.int32, (B + 1,)),
-          _dense("kv_len", kv_len, q, torch.int32, (B,)), B, T, Hq, Hk, d, k_cache.shape[0], k_cache.shape[1], width,
-          int(bool(causal)), float(sm_scale), dtype)
+    B, width = table = page_table.shape
+    _call(get_lib().sage_paged_attn, "sage_paged_attn", dev, stream, qp, kp, vp, op, qs, ks, vs, os_,
+          _dense("page_table", page_table, q, dev, torch.int32, table),
+          _dense("cu_q", cu_q, q, dev, torch.int32, (B + 1,)), _dense("kv_len", kv_len, q, dev, torch.int32, (B,)),
+          B, T, Hq, Hk, d, pages, size, width, int(bool(causal)), float(sm_scale), code)
 
 
 def sageattn_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, causal: bool = True,
@@ -643,17 +646,18 @@ def sageattn_paged(q, k_cache, v_cache, page_table, cu_q, kv_len, causal: bool =
 def sage_cross_attn(q, k, v, o, key_len, sm_scale: float, stream=None) -> None:
     """Cross attention of q [B, Hq, Nq, d] to k, v [B, Hk, Nk, d] into o [B, Hq, Nq, d]; key_len int32 [B]
     (None: all Nk): keys past it are not used.  Strided views with contiguous channels."""
-    dtype = _activations(q, 4, "a [B, H, N, d] tensor")
-    B, Hq, Nq, d = q.shape
+    dev, dt, code = _activations(q, 4, "a [B, H, N, d] tensor")
+    B, Hq, Nq, d = shape = q.shape
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a [B, Hk, Nk, d] tensor")
-    Hk, Nk = k.shape[1], k.shape[2]
-    qp, qs = _view("q", q, q, None, (0, 1, 2))
-    kp, ks = _view("k", k, q, (B, Hk, Nk, d), (0, 1, 2))
-    vp, vs = _view("v", v, q, (B, Hk, Nk, d), (0, 1, 2))
-    op, os_ = _view("o", o, q, q.shape, (0, 1, 2))
-    _call(get_lib().sage_cross_attn, "sage_cross_attn", q.device, stream, qp, kp, vp, op, qs, ks, vs, os_,
-          _dense("key_len", key_len, q, torch.int32, (B,)), B, Hq, Hk, Nq, Nk, d, float(sm_scale), dtype)
+    _, Hk, Nk, _ = k.shape
+    keys = (B, Hk, Nk, d)
+    qp, qs = _view("q", q, q, dev, dt, shape, 0, 1, 2)
+    kp, ks = _view("k", k, q, dev, dt, keys, 0, 1, 2)
+    vp, vs = _view("v", v, q, dev, dt, keys, 0, 1, 2)
+    op, os_ = _view("o", o, q, dev, dt, shape, 0, 1, 2)
+    _call(get_lib().sage_cross_attn, "sage_cross_attn", dev, stream, qp, kp, vp, op, qs, ks, vs, os_,
+          _dense("key_len", key_len, q, dev, torch.int32, (B,)), B, Hq, Hk, Nq, Nk, d, float(sm_scale), code)
 
 
 def sageattn_cross(q, k, v, key_len=None, sm_scale: float | None = None, stream=None) -> torch.Tensor:
