@@ -136,7 +136,8 @@ int run_step(const sage::Attn16Launch& t, cudaStream_t st) {
 }
 
 // Pairs of query tiles: many items are dealt out whole, few have their key tiles cut into equal shares (of 512
-// keys at least).
+// keys at least).  16 sequences of up to 333 tokens over up to 4099 keys, 2.4 items per SM: 152 us cut, 177 us whole (the
+// last round is not full); 2 x 4096 tokens over 6001 keys, 6.9 per SM: 720 us cut (parts and joins), 643 us whole.
 int run_pair(sage::Attn16Launch& l, cudaStream_t st) {
   sage::Attn16Args& a = l.a;
   const int sms = sm_count();
