@@ -456,15 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __device__ __forceinline__ int n(int t) const { return t ? n1 : n0; }
       };
       int posted = 0;
-      auto next_steps = [&](Steps& g) -> bool {  // the next segment that has keys to read
+      // The next segment, whether or not it has keys to read.  (Not the next one that has: the posts in between come
+      // only when those before are free, and the softmax warps hold on to theirs until this warp has gone on.)
+      auto next_steps = [&](Steps& g) -> bool {
         PairSegment x;
-        while (read_post(posted, x)) {
-          ++posted;
-          g = Steps{x.n0, x.n1, x.steps, x.kv - x.first * 128};
-          if (x.steps > 0) return true;
-        }
-        g = Steps{0, 0, 0, 0};
-        return false;
+        const bool more = read_post(posted, x);
+        ++posted;
+        g = more ? Steps{x.n0, x.n1, x.steps, x.kv - x.first * 128} : Steps{0, 0, 0, 0};
+        return more;
       };
       Steps seg, ahead;
       int base = 0;                // ring fill of the segment's first K; step it: K base + 2 it, V base + 2 it + 1
@@ -522,10 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const std::integral_constant<int, 0> s0{};
       const std::integral_constant<int, 1> s1{};
       bool more = next_steps(seg), ok = true;
-      if (more && seg.n0 > 0) ok = issue_qk(seg, base, s0, 0);
-      if (more && ok && seg.n1 > 0) ok = issue_qk(seg, base, s1, 0);
+      bool begun = false;  // the segment's first scores are issued
       while (more && ok) {
+        if (!begun && seg.n0 > 0) ok = issue_qk(seg, base, s0, 0);
+        if (!begun && ok && seg.n1 > 0) ok = issue_qk(seg, base, s1, 0);
         more = next_steps(ahead);
+        begun = seg.steps > 0;  // for the next one: by this one's last step
         int it = 0;
         // the bulk of a segment: both streams have this tile and the next two, none of the rest applies
         for (; ok && it + 2 < min(seg.n0, seg.n1); ++it) {

@@ -147,3 +147,20 @@ def test_binding_refuses(sa):
         sa.sageattn_cross(q, k[:, :1].expand(1, 2, 9, 64), k)  # heads that share memory: stride 0
     with pytest.raises(sa.SageError):
         sa.sageattn_cross(q, k, k, sm_scale=0.0)
+
+
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("B,Hq,Hk,Nq,Nk,d,lengths", [
+    (3, 128, 8, 128, 5000, 64, [977, 0, 5000]),   # 64 pairs of query tiles without a key between others, cut axis
+    (3, 128, 8, 128, 5000, 128, [977, 0, 5000]),
+    (9, 32, 16, 500, 700, 128, [0, 0, 700, 0, 0, 0, 0, 0, 1]),
+    (40, 40, 40, 300, 200, 64, [200 if b in (0, 17, 38) else 0 for b in range(40)]),  # dealt out whole
+    (40, 40, 40, 300, 200, 128, [200 if b in (0, 17, 38) else 0 for b in range(40)]),
+])
+def test_long_runs_of_items_without_keys(sa, dt, B, Hq, Hk, Nq, Nk, d, lengths):
+    g = torch.Generator().manual_seed(7)
+    q = torch.randn(B, Nq, Hq, d, generator=g).to(DT[dt]).cuda().transpose(1, 2)
+    k, v = torch.randn(2, B, Hk, Nk, d, generator=g).to(DT[dt]).cuda()
+    o = sa.sageattn_cross(q, k, v, torch.tensor(lengths, dtype=torch.int32, device="cuda"), 0.2)
+    assert sa.sage_last_device_error() == 0
+    check(o, q, k, v, lengths, 0.2)

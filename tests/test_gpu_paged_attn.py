@@ -297,3 +297,18 @@ def test_video_block(sa):
     for b, n in enumerate((77, 30)):
         seen = torch.ones(N, n, dtype=torch.bool, device="cuda")
         assert_attention(o[b], *attend(x[b], text[0][b, :, :n], text[1][b, :, :n], seen, d ** -0.5))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seqs", [
+    [(150, 1000)] + [(150, 0)] * 20 + [(150, 2000)],
+    [(700, 300)] * 5 + [(400, 1)] * 40 + [(30, 1000)],  # causal: most tokens see no key
+    [(260, 0)] * 300 + [(260, 500)] + [(260, 0)] * 100 + [(1, 77)],
+], ids=["empty_between", "more_new_than_keys", "many_empty"])
+def test_long_runs_of_items_without_keys(sa, seqs, d, causal):
+    p, keys, values, cu = problem(seqs, 4, 2, d, 64, torch.bfloat16)
+    o = run(sa, p, causal, 0.1)
+    assert sa.sage_last_device_error() == 0
+    check(o, p, seqs, keys, values, cu, causal, 0.1)
+    assert (o[cu[-1]:] == 99.0).all()
