@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         g = more ? Steps{x.n0, x.n1, x.steps, x.kv - x.first * 128} : Steps{0, 0, 0, 0};
         return more;
       };
-      Steps seg, ahead;
+      Steps seg{0, 0, 0, 0}, ahead;
       int base = 0;                // ring fill of the segment's first K; step it: K base + 2 it, V base + 2 it + 1
       int scores[2] = {0, 0};      // score tiles issued for each stream so far
       int weights[2] = {0, 0};     // weight tiles used
@@ -520,13 +520,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const std::integral_constant<int, 0> s0{};
       const std::integral_constant<int, 1> s1{};
-      bool more = next_steps(seg), ok = true;
-      bool begun = false;  // the segment's first scores are issued
+      // (it begins behind a segment without steps, whose turn issues the first scores of the one behind it)
+      bool more = true, ok = true;
       while (more && ok) {
-        if (!begun && seg.n0 > 0) ok = issue_qk(seg, base, s0, 0);
-        if (!begun && ok && seg.n1 > 0) ok = issue_qk(seg, base, s1, 0);
         more = next_steps(ahead);
-        begun = seg.steps > 0;  // for the next one: by this one's last step
         int it = 0;
         // the bulk of a segment: both streams have this tile and the next two, none of the rest applies
         for (; ok && it + 2 < min(seg.n0, seg.n1); ++it) {
@@ -550,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (OWN_P) ok = qk(s0) && pv(s0) && qk(s1) && pv(s1);
           else ok = pv(s0) && qk(s0) && pv(s1) && qk(s1);
         }
-        for (; ok && it < seg.steps; ++it) {
-          const bool last = it + 1 == seg.steps;
+        for (; ok && it < max(seg.steps, 1); ++it) {
+          const bool last = it + 1 >= seg.steps;
           auto turn = [&](auto t) -> bool {
             // what follows: the stream's next step, or, in the segment's last step, the next segment's first
             auto follow = [&]() -> bool {
