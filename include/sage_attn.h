@@ -403,9 +403,11 @@ int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* 
  * page_table: [B][pages_per_seq]; cu_q: [B+1], ascending; kv_len: [B].  Hq is a multiple of Hk, at most
  * 128 times it.  Values of kv_len are taken into [0, pages_per_seq * page_size], of cu_q into [0, T];
  * a page outside the cache reads as zeros.  Cache rows past a sequence's end are never used, whatever
- * they hold.  When few tokens meet long caches the key axis is split over CTAs and joined (fp32
- * parts in a stream-ordered workspace), in a fixed order: the same call gives the same bits.  A table
- * for more than 2^24 keys, or more than 2^24 sequences: SAGE_ERR_UNSUPPORTED.  A cu_q that is not
+ * they hold; a value that is not finite among a sequence's own kv_len[b] may reach the tokens that do
+ * not see it too (their weight for it is 0, and 0 * inf is NaN).  When few tokens meet long caches the
+ * key axis is split over CTAs and joined (fp32 parts in a stream-ordered workspace), in a fixed order: the
+ * same call gives the same bits.  A table for more than 2^24 keys, or more than 2^24 sequences:
+ * SAGE_ERR_UNSUPPORTED.  A cu_q that is not
  * ascending leaves unspecified rows of o, never an access outside the tensors. */
 int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, void* o, const sage_strides* q_st,
                     const sage_strides* k_cache_st, const sage_strides* v_cache_st, const sage_strides* o_st,

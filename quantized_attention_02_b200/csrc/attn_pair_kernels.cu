@@ -460,10 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // only when those before are free, and the softmax warps hold on to theirs until this warp has gone on.)
       auto next_steps = [&](Steps& g) -> bool {
         PairSegment x;
-        const bool more = read_post(posted, x);
+        if (!read_post(posted, x)) {
+          g = Steps{0, 0, 0, 0};
+          return false;
+        }
         ++posted;
-        g = more ? Steps{x.n0, x.n1, x.steps, x.kv - x.first * 128} : Steps{0, 0, 0, 0};
-        return more;
+        g = Steps{x.n0, x.n1, x.steps, x.kv - x.first * 128};
+        return true;
       };
       Steps seg{0, 0, 0, 0}, ahead;
       int base = 0;                // ring fill of the segment's first K; step it: K base + 2 it, V base + 2 it + 1
@@ -520,8 +523,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       const std::integral_constant<int, 0> s0{};
       const std::integral_constant<int, 1> s1{};
-      // (it begins behind a segment without steps, whose turn issues the first scores of the one behind it)
-      bool more = true, ok = true;
+      // (a segment without steps still has a turn, which issues the first scores of the one behind it)
+      bool more = next_steps(seg), ok = true;
+      if (more && seg.n0 > 0) ok = issue_qk(seg, base, s0, 0);
+      if (more && ok && seg.n1 > 0) ok = issue_qk(seg, base, s1, 0);
       while (more && ok) {
         more = next_steps(ahead);
         int it = 0;
