@@ -404,7 +404,8 @@ int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* 
  * 128 times it.  Values of kv_len are taken into [0, pages_per_seq * page_size], of cu_q into [0, T];
  * a page outside the cache reads as zeros.  Cache rows past a sequence's end are never used, whatever
  * they hold; a value that is not finite among a sequence's own kv_len[b] may reach the tokens that do
- * not see it too (their weight for it is 0, and 0 * inf is NaN).  When few tokens meet long caches the
+ * not see it too (their weight for it is 0, and 0 * inf is NaN).  A score of NaN or +inf makes its token's
+ * row NaN, one of -inf has no weight, and a row with no other scores is 0.  When few tokens meet long caches the
  * key axis is split over CTAs and joined (fp32 parts in a stream-ordered workspace), in a fixed order: the
  * same call gives the same bits.  A table for more than 2^24 keys, or more than 2^24 sequences:
  * SAGE_ERR_UNSUPPORTED.  A cu_q that is not
@@ -418,7 +419,8 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
 /* Cross attention to states of another length: o_i = sum_j softmax_j(q_i . k_j * sm_scale) v_j over the
  * keys j < key_len[b] (all Nk when key_len is NULL; values are taken into [0, Nk]).  No key: 0.
  * q, o: [B,Hq,Nq,d]; k, v: [B,Hk,Nk,d] (may be NULL when Nk = 0); query head h uses key head
- * h / (Hq/Hk); Hq as above.  Keys past key_len are never used, whatever they hold.  Nq = 1 is a
+ * h / (Hq/Hk); Hq as above.  Keys past key_len are never used, whatever they hold; scores that are not
+ * finite as above.  Nq = 1 is a
  * decoder's single token.  More than 2^24 keys: SAGE_ERR_UNSUPPORTED. */
 int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const sage_strides* q_st,
                     const sage_strides* k_st, const sage_strides* v_st, const sage_strides* o_st,

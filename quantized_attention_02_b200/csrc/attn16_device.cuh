@@ -57,6 +57,9 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   }
 }
 
+// What a row's O is multiplied with at the end: 0 for a row without a key, NaN for a sum that is NaN.
+__device__ __forceinline__ float weight_sum_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 // Parts c0 .. c1 of ROWS rows joined by a warp, in the parts' order: acc[k][e] = sum_c 2^(m_c - m) O_c of row k, l
 // likewise, m the largest m_c.  at(k, c): the place of part c of row k in ml and in o (rows of D = 32 C fp32).
 // The lanes take the parts' factors first, 32 at a time, so that the loads of O follow each other without
@@ -115,7 +118,7 @@ __device__ __forceinline__ void join_parts(float (&acc)[ROWS][C], float (&l)[ROW
 // A joined row into O: this lane's C channels from `dst` on.
 template <bool BF16, int C>
 __device__ __forceinline__ void store_joined(uint16_t* dst, const float (&acc)[C], float l) {
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = weight_sum_inverse(l);
 #pragma unroll
   for (int e = 0; e < C; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
 }

@@ -31,9 +31,12 @@ struct RowState {
 #pragma unroll
     for (int i = 0; i < 4; ++i) lsum[i] = make_float2(0.f, 0.f);
   }
+  // NaN where a score was NaN or +inf (the accumulator may have missed it).  0 where no score was above -inf: what the
+  // polynomial's 2^-126 left in the sum, and in the accumulator, does not count.
   __device__ __forceinline__ float sum() const {
     const float2 l2 = __fadd2_rn(__fadd2_rn(lsum[0], lsum[1]), __fadd2_rn(lsum[2], lsum[3]));
-    return l2.x + l2.y;
+    const float l = l2.x + l2.y;
+    return m_use > -INFINITY || l != l ? l : 0.f;
   }
 };
 
@@ -43,6 +46,8 @@ constexpr float kWeightShift = BF16 ? 0.f : 7.f;
 
 // Weights 2^(s * scale - offset) of 32 scores into TMEM at tP, one pair in POLY by the polynomial (0: none; the
 // MUFU pipe alone would hold up the rest, more of it costs more issue slots than it saves), and their sums.
+// NaN and +inf make the sum NaN: on the MUFU pipe by the weight (inf - inf is NaN once the offset has followed), beside the
+// polynomial, whose result for them is some number, by adding 0 * u.
 template <bool BF16, int POLY>
 __device__ __forceinline__ void weights32(const uint32_t* x, uint32_t tP, float scale_log2, float off, float2 (&sum)[4]) {
   const float2 sc2 = make_float2(scale_log2, scale_log2), off2 = make_float2(off, off);
@@ -51,8 +56,13 @@ __device__ __forceinline__ void weights32(const uint32_t* x, uint32_t tP, float 
   for (int i = 0; i < 32; i += 2) {
     const float2 u = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), sc2, off2);
     float2 p;
-    if (POLY > 0 && (i >> 1) % (POLY > 0 ? POLY : 1) == POLY - 1) p = exp2_poly2(u);
-    else p = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+    if (POLY > 0 && (i >> 1) % (POLY > 0 ? POLY : 1) == POLY - 1) {
+      const float2 t = make_float2(max_nan(u.x, -126.f), max_nan(u.y, -126.f));
+      p = exp2_poly2_above(t);
+      sum[(i >> 1) & 3] = __ffma2_rn(t, make_float2(0.f, 0.f), sum[(i >> 1) & 3]);
+    } else {
+      p = make_float2(fast_exp2(u.x), fast_exp2(u.y));
+    }
     sum[(i >> 1) & 3] = __fadd2_rn(sum[(i >> 1) & 3], p);
     pk[i >> 1] = pack16<BF16>(p.x, p.y);
   }
@@ -78,6 +88,7 @@ __device__ __forceinline__ float scores_max(const uint32_t* x) {
 // row's first tile.  s_free (kOwnWeights): receives an arrival once the scores are read for the last time; prior:
 // waits until the product that read the last weights is done, false if that wait gave up.  On return the
 // weights are stored but not yet waited for (tcgen05.wait::st).
+// Scores that are not finite: NaN and +inf make the row NaN, -inf has no weight, in every tile and at every place of it.
 template <int D, bool BF16, typename Prior>
 __device__ __forceinline__ bool softmax_tile(RowState& row, uint32_t tS, uint32_t tO, uint32_t tP, int seen, int seen_warp,
                                              int seen_most, bool fresh, float scale_log2, uint64_t* s_free, Prior prior) {

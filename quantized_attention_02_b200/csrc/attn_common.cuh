@@ -36,17 +36,23 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return r;
 }
 
+// The larger of two, NaN if one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // exp2 on the FMA pipe for a pair of arguments (Cody-Waite style range reduction plus a
 // polynomial), to take part of the exp2 work off the MUFU unit:
 //   t -> max(t, -126); n = round_to_nearest(t) via the 1.5 * 2^23 add; f = t - n in [-1/2, 1/2];
 //   2^f ~ c0 + c1 f + c2 f^2 + c3 f^3 with coefficients fitted here to the minimax relative error on
 //   [-1/2, 1/2] (max relative error 7.5e-5, below half an fp16 ulp); 2^n by adding n to the
 //   exponent field (n << 23, taken from the low bits of the magic sum).
-__device__ __forceinline__ float2 exp2_poly2(float2 t) {
+// exp2_poly2_above: for arguments of -126 at least (a NaN gives some number).
+__device__ __forceinline__ float2 exp2_poly2_above(float2 t) {
   constexpr float c0 = 0.9999281167984009f, c1 = 0.6932609677314758f, c2 = 0.2426108568906784f,
                   c3 = 0.055171459913253784f;
-  t.x = fmaxf(t.x, -126.f);
-  t.y = fmaxf(t.y, -126.f);
   const float2 y = __fadd2_rn(t, make_float2(kMagicF, kMagicF));
   const float2 n = __fadd2_rn(y, make_float2(-kMagicF, -kMagicF));
   const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), t);
@@ -55,6 +61,10 @@ __device__ __forceinline__ float2 exp2_poly2(float2 t) {
   p = __ffma2_rn(p, f, make_float2(c0, c0));
   return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(y.x) << 23)),
                      __int_as_float(__float_as_int(p.y) + (__float_as_int(y.y) << 23)));
+}
+
+__device__ __forceinline__ float2 exp2_poly2(float2 t) {
+  return exp2_poly2_above(make_float2(fmaxf(t.x, -126.f), fmaxf(t.y, -126.f)));
 }
 
 template <uint32_t N>

@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = seg->tok0 + r_tok;
         const bool row_valid = r < a.tile_tokens * a.G && tok < sq.nq;
         const bool whole = seg->whole;
-        const float scale = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const float scale = whole ? weight_sum_inverse(l) : 1.f;
         uint16_t* orow = static_cast<uint16_t*>(a.o) + out_offset(a, sq, tok, seg->hk * a.G + r_head);
         const long long part = static_cast<long long>(seg->part) * kRows + t * 128 + r;
         if (!whole && row_valid) a.part_ml[part] = make_float2(row.m_use, l);

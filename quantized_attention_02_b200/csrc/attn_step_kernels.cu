@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float v = (y.x + y.y) + (y.z + y.w);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if (lane == 0) sRed[r] = seg.whole ? (v > 0.f ? 1.f / v : 0.f) : v;
+        if (lane == 0) sRed[r] = seg.whole ? weight_sum_inverse(v) : v;
       }
       group_sync();
       if (c < D && ok && !*abort_flag) {

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (ok && !*abort_flag && t == 0 && warp_live) {
       const bool whole = range.parts == 1;  // else: a part, joined by attn_tile_join_kernel
-      const float scale = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+      const float scale = whole ? weight_sum_inverse(l) : 1.f;
       uint16_t* orow = static_cast<uint16_t*>(a.o) + out_offset(a, seq, tok, hk * a.G + r % a.G);
       const long long part = static_cast<long long>(blockIdx.x) * 128 + r;
       if (!whole && row_valid) a.part_ml[part] = make_float2(row.m_use, l);
