@@ -407,7 +407,7 @@ int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* 
  * not see it too (their weight for it is 0, and 0 * inf is NaN).  A score of NaN or +inf makes its token's
  * row NaN, one of -inf has no weight, and a row with no other scores is 0.  When few tokens meet long caches the
  * key axis is split over CTAs and joined (fp32 parts in a stream-ordered workspace), in a fixed order: the
- * same call gives the same bits.  A table for more than 2^24 keys, or more than 2^24 sequences:
+ * same call gives the same bits.  A table for more than 2^24 keys, or more than 2^20 sequences:
  * SAGE_ERR_UNSUPPORTED.  A cu_q that is not
  * ascending leaves unspecified rows of o, never an access outside the tensors. */
 int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, void* o, const sage_strides* q_st,

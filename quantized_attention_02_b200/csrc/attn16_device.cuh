@@ -46,6 +46,25 @@ __device__ __forceinline__ long long out_offset(const Attn16Args& a, const Seque
   return (a.cu_q ? 0 : s.b * a.o_sb) + h * a.o_sh + static_cast<long long>(s.token0 + tok) * a.o_sn;
 }
 
+// Paged: how many sequences own slots up to `slot`, where sequence b owns those from cu_q[b] / tokens + b on (tokens: of
+// a slot).  That leaves room for its ceil(nq / tokens) slots before the next one's and needs no sum over the sequences.
+// By a whole warp.  The places ascend, so each look at 32 of them leaves one piece in 32: a look at every place took
+// 700 cycles per 32 sequences, and a walk past many empty ones could then outlast the waits for it (the square of their
+// number: 30 ms for 20000, 0.5 ms now).  (Places that do not ascend give some number in [0, B].)
+__device__ __forceinline__ int sequences_upto(const Attn16Args& a, int tokens, int slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.B;  // the number is in [lo, lo + n]
+  while (n > 0) {
+    const int piece = (n + 31) >> 5, at = lane * piece;
+    const int last = lo + min(n, at + piece) - 1;  // of this lane's piece
+    const bool in = at < n && min(max(__ldg(a.cu_q + last), 0), a.Nq) / tokens + last <= slot;
+    const int skip = min(n, __popc(__ballot_sync(0xffffffffu, in)) * piece);
+    lo += skip;
+    n = max(0, min(piece, n - skip) - 1);  // the next piece, whose last is past the slot
+  }
+  return lo;
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   if constexpr (BF16) {

@@ -93,9 +93,7 @@ struct __align__(16) PairSegment {
 };
 static_assert(sizeof(PairSegment) == 64, "posted as four 16-byte pieces");
 
-// Tile slot -> pair p of sequence b.  Paged: sequence b owns the slots from cu_q[b] / cta_tokens + b on, which
-// leaves room for its ceil(nq / cta_tokens) pairs before the next one's and needs no sum over the sequences;
-// some slots have no pair (false).  By a whole warp.
+// Slot -> pair p of sequence b; some slots have no pair (false).  By a whole warp.
 __device__ __forceinline__ bool slot_pair(const Attn16Args& a, int slot, Sequence& seq, int& p) {
   const int cta_tokens = 2 * a.tile_tokens;
   if (!a.cu_q) {
@@ -104,12 +102,7 @@ __device__ __forceinline__ bool slot_pair(const Attn16Args& a, int slot, Sequenc
     p = slot % per_b;
     return true;
   }
-  int upto = 0;
-  for (int base = 0; base < a.B; base += 32) {
-    const int i = base + static_cast<int>(threadIdx.x & 31);
-    const bool in = i < a.B && min(max(__ldg(a.cu_q + i), 0), a.Nq) / cta_tokens + i <= slot;
-    upto += __popc(__ballot_sync(0xffffffffu, in));
-  }
+  const int upto = sequences_upto(a, cta_tokens, slot);
   if (upto == 0) return false;
   seq = sequence(a, upto - 1);
   p = slot - (seq.token0 / cta_tokens + seq.b);

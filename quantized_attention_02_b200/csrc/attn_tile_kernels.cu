@@ -62,17 +62,10 @@ __device__ __forceinline__ KeyRange key_range(int nt, int splits, int min_chunk,
   return r;
 }
 
-// Tile slot -> sequence and first token.  Paged: sequence b owns the slots from cu_q[b] / tile_tokens + b on, which
-// leaves room for its ceil(nq / tile_tokens) tiles before the next one's and needs no sum over the sequences;
-// some slots have no tile (false).  By a whole warp.
+// Tile slot -> sequence and first token; some slots have no tile (false).  By a whole warp.
 __device__ __forceinline__ bool tile_of_slot(const Attn16Args& a, int slot, Sequence& seq, int& tok0) {
   if (a.cu_q) {
-    int upto = 0;
-    for (int base = 0; base < a.B; base += 32) {
-      const int i = base + static_cast<int>(threadIdx.x & 31);
-      const bool in = i < a.B && min(max(__ldg(a.cu_q + i), 0), a.Nq) / a.tile_tokens + i <= slot;
-      upto += __popc(__ballot_sync(0xffffffffu, in));
-    }
+    const int upto = sequences_upto(a, a.tile_tokens, slot);
     if (upto == 0) return false;
     seq = sequence(a, upto - 1);
     tok0 = (slot - (seq.token0 / a.tile_tokens + seq.b)) * a.tile_tokens;

@@ -171,8 +171,10 @@ int run_tile(sage::Attn16Launch& l, int64_t ctas, cudaStream_t st) {
   return part_free(ws, cuda_status(sage::launch_attn_tile(l, st)), st);
 }
 
-// Keys of a sequence: no wait inside the kernels then comes near their limit.
+// Keys of a sequence, and sequences: no wait inside the kernels then comes near their limit of 2^30 cycles.  2^24 keys are
+// 2^17 key tiles of 1500 to 4000 cycles; a role that walks past 2^20 empty sequences takes at most 600 for each.
 constexpr int64_t kMaxKeys = 1 << 24;
+constexpr int kMaxSequences = 1 << 20;
 
 // Which kernel: by the rows (tokens x group) that a key head of an average sequence has.
 bool few_rows(int64_t tokens, int64_t sequences, int G) {
@@ -262,7 +264,7 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
       !view_ok(o, o_st, 1, Hq, T) || !view_ok(k_cache, k_cache_st, num_pages, Hk, page_size) ||
       !view_ok(v_cache, v_cache_st, num_pages, Hk, page_size))
     return SAGE_ERR_INVALID;
-  if (static_cast<int64_t>(pages_per_seq) * page_size > kMaxKeys || B > (1 << 24) ||
+  if (static_cast<int64_t>(pages_per_seq) * page_size > kMaxKeys || B > kMaxSequences ||
       static_cast<int64_t>(T) * Hq >= (1ll << 31) || !strides_fit(q_st) || !strides_fit(k_cache_st) ||
       !strides_fit(v_cache_st))
     return SAGE_ERR_UNSUPPORTED;

@@ -312,3 +312,42 @@ def test_long_runs_of_items_without_keys(sa, seqs, d, causal):
     assert sa.sage_last_device_error() == 0
     check(o, p, seqs, keys, values, cu, causal, 0.1)
     assert (o[cu[-1]:] == 99.0).all()
+
+
+# ------------------------------------------------------------------ many sequences, nearly all of them empty
+@pytest.mark.parametrize("B", [31, 32, 33, 64, 65, 1024, 1025, 1056, 1057, 7000])
+@pytest.mark.parametrize("rows", ["tile", "pair"])
+def test_few_among_many_sequences(sa, B, rows):
+    # the place of a slot's sequence is looked up among B: first, last and some in between have tokens
+    G, d = 8, 64
+    # the average rows of a sequence choose the kernel: 17 to 128 of them, or more
+    total = -(-B * (40 if rows == "tile" else 140) // G)
+    at = sorted({0, B // 3, B // 2, B // 2 + 1, B - 1})
+    seqs = [(0, 10)] * B
+    for n, b in enumerate(at):
+        seqs[b] = (total // len(at) + (total % len(at) if n == 0 else 0), 65 + 100 * n)
+    p, keys, values, cu = problem(seqs, G, 1, d, 64, torch.float16, seed=B)
+    o = run(sa, p, False, 0.1)
+    check(o, p, seqs, keys, values, cu, False, 0.1)
+    assert (o[cu[-1]:] == 99).all()
+
+
+def test_a_walk_past_many_empty_sequences_is_short(sa):
+    # 20000 sequences of which the first has all tokens; a walk that looks at all sequences for each slot takes 30 ms
+    B, T = 20000, 322500
+    q = torch.zeros(T, 8, 64, dtype=torch.float16, device="cuda")
+    cache = torch.ones(2, 64, 1, 64, dtype=torch.float16, device="cuda")
+    cu = torch.full((B + 1,), T, dtype=torch.int32, device="cuda")
+    cu[0] = 0
+    kv = torch.full((B,), 100, dtype=torch.int32, device="cuda")
+    table = torch.zeros(B, 2, dtype=torch.int32, device="cuda")
+    times = []
+    for _ in range(4):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        o = sa.sageattn_paged(q, cache, cache, table, cu, kv, False)
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end))
+    assert (o == 1).all()
+    assert min(times) < 10

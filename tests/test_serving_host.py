@@ -153,3 +153,7 @@ def test_attention_refuses_strides(sa, field, value, status):
 def test_attention_without_tokens_is_no_work(sa):
     assert paged(sa, T=0, q=None, o=None) == 0 and paged(sa, B=0, table=None, cu=None, len=None) == 0
     assert cross(sa, Nq=0, q=None, o=None) == 0 and cross(sa, B=0) == 0
+
+
+def test_paged_attn_refuses_more_sequences_than_its_waits_allow(sa):
+    assert paged(sa, B=(1 << 20) + 1) == UNSUPPORTED
