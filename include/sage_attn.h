@@ -351,6 +351,7 @@ int sage_attn_fwd_host_variant(const void* q, const void* k, const void* v, void
  *     token (host memory, read during the call), the channel stride is 1.  A paged cache is the
  *     view [page][head][token in page][d] (b = page stride).  Every base pointer is 16-byte
  *     aligned; every stride of a dimension larger than 1 is positive and a multiple of 8 elements.
+ *     The attention calls take strides below 2^38 elements (a query's head stride: times Hq/Hk).
  *   - page_size is 16, 32, 64, 128 or 256 tokens; num_pages * page_size stays below 2^31.
  *   - Index arrays (positions, slots, page_table, cu_q, kv_len, key_len) are int32 device memory,
  *     dense.  Their values are not known to the host: the kernels check them as stated and never

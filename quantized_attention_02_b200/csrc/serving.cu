@@ -70,8 +70,11 @@ uint64_t map_stride(int64_t elems, int64_t extent, int d) {
   return static_cast<uint64_t>(extent > 1 ? elems : d) * 2;
 }
 
-bool strides_fit(const sage_strides* s) {  // 40-bit byte strides
-  return s->b < (1ll << 38) && s->h < (1ll << 31) && s->n < (1ll << 38);
+// Strides of a view [B][H][N][d] that a tensor map takes: below 2^40 bytes, that from one group of G heads to the next
+// too.  Of a dimension of one entry any stride does.
+bool strides_fit(const sage_strides* s, int64_t B, int64_t H, int64_t N, int64_t G) {
+  constexpr int64_t kLimit = 1ll << 38;
+  return (B == 1 || s->b < kLimit) && (N == 1 || s->n < kLimit) && (H == 1 || s->h < kLimit / G);
 }
 
 // queries [B][Hk][N][G][d] from a [B][Hq][N][d] view
@@ -264,11 +267,11 @@ int sage_paged_attn(const void* q, const void* k_cache, const void* v_cache, voi
       !view_ok(o, o_st, 1, Hq, T) || !view_ok(k_cache, k_cache_st, num_pages, Hk, page_size) ||
       !view_ok(v_cache, v_cache_st, num_pages, Hk, page_size))
     return SAGE_ERR_INVALID;
-  if (static_cast<int64_t>(pages_per_seq) * page_size > kMaxKeys || B > kMaxSequences ||
-      static_cast<int64_t>(T) * Hq >= (1ll << 31) || !strides_fit(q_st) || !strides_fit(k_cache_st) ||
-      !strides_fit(v_cache_st))
-    return SAGE_ERR_UNSUPPORTED;
   const int G = Hq / Hk;
+  if (static_cast<int64_t>(pages_per_seq) * page_size > kMaxKeys || B > kMaxSequences ||
+      static_cast<int64_t>(T) * Hq >= (1ll << 31) || !strides_fit(q_st, 1, Hq, T, G) ||
+      !strides_fit(k_cache_st, num_pages, Hk, page_size, 1) || !strides_fit(v_cache_st, num_pages, Hk, page_size, 1))
+    return SAGE_ERR_UNSUPPORTED;
   sage::Attn16Launch l{};
   sage::Attn16Args& a = l.a;
   a.o = o;
@@ -309,10 +312,10 @@ int sage_cross_attn(const void* q, const void* k, const void* v, void* o, const 
   if (B == 0 || Nq == 0) return SAGE_OK;
   if (!view_ok(q, q_st, B, Hq, Nq) || !view_ok(o, o_st, B, Hq, Nq)) return SAGE_ERR_INVALID;
   if (Nk > 0 && (!view_ok(k, k_st, B, Hk, Nk) || !view_ok(v, v_st, B, Hk, Nk))) return SAGE_ERR_INVALID;
-  if (static_cast<int64_t>(B) * Nq * Hq >= (1ll << 31) || Nk > kMaxKeys || !strides_fit(q_st) ||
-      (Nk > 0 && (!strides_fit(k_st) || !strides_fit(v_st))))
-    return SAGE_ERR_UNSUPPORTED;
   const int G = Hq / Hk;
+  if (static_cast<int64_t>(B) * Nq * Hq >= (1ll << 31) || Nk > kMaxKeys || !strides_fit(q_st, B, Hq, Nq, G) ||
+      (Nk > 0 && (!strides_fit(k_st, B, Hk, Nk, 1) || !strides_fit(v_st, B, Hk, Nk, 1))))
+    return SAGE_ERR_UNSUPPORTED;
   sage::Attn16Launch l{};
   sage::Attn16Args& a = l.a;
   a.o = o;

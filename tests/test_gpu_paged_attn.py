@@ -351,3 +351,23 @@ def test_a_walk_past_many_empty_sequences_is_short(sa):
         times.append(start.elapsed_time(end))
     assert (o == 1).all()
     assert min(times) < 10
+
+
+@pytest.mark.parametrize("new", [1, 20, 100])
+def test_heads_first_cache_with_head_strides_past_32_bits(sa, new):
+    # [Hk][pages][page][d] in memory: 2^31 elements and more from one head to the next
+    page, Hk, Hq, d, kv = 256, 2, 8, 64, 500
+    pages = (1 << 31) // (page * d) + 2
+    caches = [torch.empty(Hk, pages, page, d, dtype=torch.float16, device="cuda").permute(1, 2, 0, 3) for _ in range(2)]
+    assert caches[0].stride(2) >= 1 << 31
+    ids = torch.tensor([pages - 1, pages - 2], device="cuda")
+    k, v = torch.randn(2, kv, Hk, d, generator=torch.Generator().manual_seed(new)).half().cuda()
+    j = torch.arange(kv, device="cuda")
+    for cache, x in zip(caches, (k, v)):
+        cache[ids[j // page], j % page] = x
+    q = torch.randn(new, Hq, d, generator=torch.Generator().manual_seed(new)).half().cuda()
+    o = sa.sageattn_paged(q, *caches, ids.int()[None], torch.tensor([0, new], dtype=torch.int32, device="cuda"),
+                          torch.tensor([kv], dtype=torch.int32, device="cuda"))
+    seen = j[None] <= kv - new + torch.arange(new, device="cuda")[:, None]
+    k, v = (x.transpose(0, 1).repeat_interleave(Hq // Hk, 0) for x in (k, v))
+    assert_attention(o.transpose(0, 1), *attend(q.transpose(0, 1), k, v, seen, d ** -0.5))
