@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 
 #include "attn16_kernels.cuh"
+#include "attn_common.cuh"
 
 namespace sage {
 
@@ -79,6 +80,35 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // What a row's O is multiplied with at the end: 0 for a row without a key, NaN for a sum that is NaN.
 __device__ __forceinline__ float weight_sum_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
+// Two means of an output row as a pair, in fp16's range.  The weights' rounding moves a mean by up to 2^-11 of the values'
+// size, which their unrounded sum does not follow: next to 65504 the mean would round to infinity.  (bf16's range is
+// that of the accumulator.)
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_in_range(float lo, float hi) {
+  if constexpr (!BF16) {
+    if (fabsf(lo) < INFINITY) lo = fminf(fmaxf(lo, -65504.f), 65504.f);
+    if (fabsf(hi) < INFINITY) hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+  }
+  return pack16<BF16>(lo, hi);
+}
+// 32 of a row's means, unnormalised, times `scale` into pairs, and the largest of them into `most` (four chains).
+template <bool BF16>
+__device__ __forceinline__ void pack_means(const uint32_t (&o)[32], float scale, uint32_t (&w)[16], __half2 (&most)[4]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    w[i] = pack16<BF16>(__uint_as_float(o[2 * i]) * scale, __uint_as_float(o[2 * i + 1]) * scale);
+    if constexpr (!BF16) most[i & 3] = __hmax2(most[i & 3], __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+  }
+}
+// Whether one of the warp's rows has an infinite mean, so that they have to be packed again, in range.
+template <bool BF16>
+__device__ __forceinline__ bool out_of_range(const __half2 (&most)[4]) {
+  if constexpr (BF16) return false;
+  const __half2 m = __hmax2(__hmax2(most[0], most[1]), __hmax2(most[2], most[3]));
+  const uint32_t bits = *reinterpret_cast<const uint32_t*>(&m);
+  return __any_sync(0xffffffffu, (bits & 0xffffu) == 0x7c00u || bits >> 16 == 0x7c00u);
+}
+
 // Parts c0 .. c1 of ROWS rows joined by a warp, in the parts' order: acc[k][e] = sum_c 2^(m_c - m) O_c of row k, l
 // likewise, m the largest m_c.  at(k, c): the place of part c of row k in ml and in o (rows of D = 32 C fp32).
 // The lanes take the parts' factors first, 32 at a time, so that the loads of O follow each other without
@@ -139,7 +169,8 @@ template <bool BF16, int C>
 __device__ __forceinline__ void store_joined(uint16_t* dst, const float (&acc)[C], float l) {
   const float inv = weight_sum_inverse(l);
 #pragma unroll
-  for (int e = 0; e < C; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack16<BF16>(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < C; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = pack_in_range<BF16>(acc[e] * inv, acc[e + 1] * inv);
 }
 
 }  // namespace sage

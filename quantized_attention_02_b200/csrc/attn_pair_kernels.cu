@@ -648,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long part = static_cast<long long>(seg->part) * kRows + t * 128 + r;
         if (!whole && row_valid) a.part_ml[part] = make_float2(row.m_use, l);
         uint8_t* stage = smem + L::OFF_STAGE + (warp - 4) * 4096;  // [32 rows][8 pieces], piece p of row i at p ^ (i & 7)
+        __half2 most[4] = {};
 #pragma unroll
         for (int cb = 0; cb < D; cb += 32) {
           uint32_t ov[32];
@@ -659,9 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (whole) {
             uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack16<BF16>(__uint_as_float(ov[2 * i]) * scale, __uint_as_float(ov[2 * i + 1]) * scale);
+            pack_means<BF16>(ov, scale, w, most);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint4 v = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
@@ -674,6 +673,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
             }
+          }
+        }
+        if (out_of_range<BF16>(most)) {  // (parts have none)
+#pragma unroll 1
+          for (int cb = 0; cb < D; cb += 8) {
+            uint32_t ov[8], w[4];
+            tmem_ld8_sync(tO + cb, ov);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = pack_in_range<BF16>(__uint_as_float(ov[2 * i]) * scale, __uint_as_float(ov[2 * i + 1]) * scale);
+            const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+            if constexpr (L::STAGED) *reinterpret_cast<uint4*>(stage + lane * 128 + (((cb / 8) ^ (lane & 7)) << 4)) = v;
+            else if (row_valid) *reinterpret_cast<uint4*>(orow + cb) = v;
           }
         }
         if (L::STAGED && whole) {

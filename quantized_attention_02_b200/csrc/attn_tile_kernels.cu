@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
               *reinterpret_cast<uint4*>(orow + cb + i) =
-                  make_uint4(pack16<BF16>(o[i] * scale, o[i + 1] * scale), pack16<BF16>(o[i + 2] * scale, o[i + 3] * scale),
-                             pack16<BF16>(o[i + 4] * scale, o[i + 5] * scale), pack16<BF16>(o[i + 6] * scale, o[i + 7] * scale));
+                  make_uint4(pack_in_range<BF16>(o[i] * scale, o[i + 1] * scale), pack_in_range<BF16>(o[i + 2] * scale, o[i + 3] * scale),
+                             pack_in_range<BF16>(o[i + 4] * scale, o[i + 5] * scale), pack_in_range<BF16>(o[i + 6] * scale, o[i + 7] * scale));
           } else {
             float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + cb);
 #pragma unroll
