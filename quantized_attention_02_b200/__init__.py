@@ -550,7 +550,7 @@ def sage_qk_norm_rope(q, k, q_out, k_out, cos, sin, positions=None, q_weight=Non
         kp, ks = _view("k", k, q, dev, dt, (B, Hk, N, d), 0, 1, 2)
         kop, kos = _view("k_out", k_out, q, dev, dt, (B, Hk, N, d), 0, 1, 2)
     cp, sp, rows, rot = _tables(cos, sin, q, dev)
-    per_batch = positions is not None and positions.dim() == 2
+    per_batch = isinstance(positions, torch.Tensor) and positions.dim() == 2
     pp = _dense("positions", positions, q, dev, torch.int32, (B, N) if per_batch else (N,))
     _call(get_lib().sage_qk_norm_rope, "sage_qk_norm_rope", dev, stream, qp, kp, qop, kop, qs, ks, qos, kos,
           _dense("q_weight", q_weight, q, dev, dt, (d,)), _dense("k_weight", k_weight, q, dev, dt, (d,)), cp, sp, pp,

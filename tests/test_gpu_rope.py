@@ -197,3 +197,14 @@ def test_side_stream_and_graph(sa):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_positions_that_are_no_tensor_are_refused(sa):
+    cos, sin = tables(8, 64)
+    q = torch.randn(1, 2, 4, 64, device="cuda", dtype=torch.float16)
+    with pytest.raises(TypeError):
+        sa.qk_norm_rope(q, None, cos, sin, positions=[0, 1, 2, 3])
+    x = q[0].transpose(0, 1)
+    cache = torch.zeros(2, 16, 2, 64, device="cuda", dtype=torch.float16)
+    with pytest.raises(TypeError):
+        sa.qk_norm_rope_append(x, x, x, cos, sin, [0, 1, 2, 3], torch.zeros(4, dtype=torch.int32, device="cuda"), cache, cache)
