@@ -371,3 +371,41 @@ def test_heads_first_cache_with_head_strides_past_32_bits(sa, new):
     seen = j[None] <= kv - new + torch.arange(new, device="cuda")[:, None]
     k, v = (x.transpose(0, 1).repeat_interleave(Hq // Hk, 0) for x in (k, v))
     assert_attention(o.transpose(0, 1), *attend(q.transpose(0, 1), k, v, seen, d ** -0.5))
+
+
+# ------------------------------------------------------------------ a cu_q that is not ascending, on every path
+PATHS = {  # sequences as in problem(), Hq, Hk: rows of an average sequence (tokens x group) choose the kernel
+    "step": ([(16, 300), (16, 1000), (16, 100)], 4, 4),             # 16
+    "step_groups": ([(4, 300), (4, 700), (4, 100)], 16, 4),         # 16 in groups of four
+    "step_many": ([(n % 5, 40 + n) for n in range(300)], 4, 2),     # 4 on average, more than one scan of the sequences
+    "tile": ([(30, 300), (30, 200), (40, 400)], 4, 2),              # 67, the key axis in one part
+    "tile_split": ([(30, 1500), (30, 1000), (40, 2000)], 4, 2),     # 67, in parts that are joined
+    "tile_many": ([(20 + n % 9, 50 + n) for n in range(60)], 4, 2),  # 48
+    "pair_cut": ([(100, 100), (200, 200), (100, 300)], 4, 2),       # 267, few items
+    "pair_whole": ([(100, 100), (200, 200), (100, 300)], 384, 6),   # 8533, 618 items: dealt out whole
+    "pair_many": ([(80 + n % 9, 50 + n) for n in range(60)], 16, 8),  # 168, more items than four per SM
+}
+
+
+@pytest.mark.parametrize("order", ["falling", "outside", "mixed"])
+@pytest.mark.parametrize("path", list(PATHS))
+def test_any_cu_q_stays_inside(sa, path, order):
+    seqs, Hq, Hk = PATHS[path]
+    p, keys, values, cu = problem(seqs, Hq, Hk, 64, 32, torch.float16, tail=0)
+    T, B = cu[-1], len(seqs)
+    good = run(sa, p, True, 0.125)
+    r = torch.Generator().manual_seed(B)
+    p["cu_q"] = {
+        "falling": torch.linspace(T, 0, B + 1).int(),
+        "outside": torch.tensor([-2 ** 31, 2 ** 31 - 1, -7, T + 3], dtype=torch.int32).repeat(B)[:B + 1],
+        "mixed": torch.randint(-T // 4, T + T // 4, (B + 1,), generator=r, dtype=torch.int32),
+    }[order].cuda()
+    buf = torch.full((T + 200, Hq, 64), 3.0, dtype=torch.float16, device="cuda")
+    for causal in (True, False):
+        sa.sage_paged_attn(p["q"], p["k_cache"], p["v_cache"], buf[100:T + 100], p["page_table"], p["cu_q"], p["kv_len"],
+                           causal, 0.125)
+    torch.cuda.synchronize()
+    assert (buf[:100] == 3).all() and (buf[T + 100:] == 3).all()
+    assert sa.sage_last_device_error() == 0
+    p["cu_q"] = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    assert torch.equal(run(sa, p, True, 0.125), good)
