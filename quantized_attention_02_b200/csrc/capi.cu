@@ -189,6 +189,18 @@ bool encode_tiled_16bit(CUtensorMap* map, bool bf16, const void* base, int rank,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+namespace {
+
+// While it lives, calls that a stream capture forbids are open to this thread (a capture in the global mode, of any
+// thread, otherwise refuses them and is itself broken by the attempt).  Creating a pool has nothing to do with the stream.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+}  // namespace
+
 cudaError_t workspace_alloc(void** p, size_t bytes, cudaStream_t st) {
   constexpr int kMaxDevices = 64;
   static std::mutex mu;
@@ -201,6 +213,7 @@ cudaError_t workspace_alloc(void** p, size_t bytes, cudaStream_t st) {
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!pools[dev]) {
+      RelaxedCapture relaxed;
       cudaMemPoolProps props{};
       props.allocType = cudaMemAllocationTypePinned;
       props.handleTypes = cudaMemHandleTypeNone;
