@@ -39,8 +39,8 @@ SOURCES = {
     "serving.cu": [],
 }
 HEADERS = ["sm100_ptx.cuh", "attn_kernels.cuh", "attn_v3.cuh", "prep_kernels.cuh", "workspace.cuh",
-           "sparse_kernels.cuh", "fp4_codes.cuh", "attn_fp4.cuh", "rope_kernels.cuh", "attn_common.cuh", "attn16_kernels.cuh",
-           "attn16_device.cuh", "attn16_softmax.cuh",            "tensor_map.cuh"]
+           "sparse_kernels.cuh", "fp4_codes.cuh", "attn_fp4.cuh", "rope_kernels.cuh", "attn_common.cuh",
+           "attn16_kernels.cuh", "attn16_device.cuh", "attn16_softmax.cuh", "tensor_map.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -20,7 +20,7 @@
 // CTA: 12 warps, 512 TMEM columns, about 226 KB of shared memory.
 //   warp 0      TMA: Q tiles, K and V tiles of 128 keys through one ring, K0 V0 K1 V1 ...
 //   warp 1      MMA issuer of both streams; allocates TMEM
-//   warp 2      walks through the share and posts its segments to the other warps (Board)
+//   warp 2      walks through the share and posts its segments to the other warps (PairSegment)
 //   warps 4-7   softmax and output of stream 0 (thread = query row = TMEM lane), warps 8-11 of stream 1
 #include <cuda.h>
 #include <cuda_bf16.h>

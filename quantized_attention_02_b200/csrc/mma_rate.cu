@@ -21,8 +21,8 @@
 #include "sage_attn.h"
 
 namespace sage {
-// sm100_ptx.cuh defines the device status word, so it is included in one translation unit
-// only; the probe keeps its own copies of the few wrappers it needs.
+// The probe keeps its own copies of the few wrappers it needs: what it measures does not change with the
+// kernels' helpers, and its status goes to the caller's memory instead of the device status word of sm100_ptx.cuh.
 namespace probe {
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

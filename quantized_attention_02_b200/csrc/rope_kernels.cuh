@@ -7,7 +7,7 @@
 
 namespace sage {
 
-// One of the up to three tensors a launch walks: heads [head0, head0 + heads) of the launch's head axis.
+// One of the up to three tensors a launch walks.
 struct RopeTensor {
   const void* in;
   void* out;

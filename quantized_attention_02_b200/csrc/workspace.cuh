@@ -1,5 +1,5 @@
-// workspace.cuh -- stream-ordered device workspace for the entry points that need one
-// (sage_attn_fwd, sage_attn_fwd_host).
+// workspace.cuh -- stream-ordered device workspace for the entry points that need one: the forward passes, the
+// preparation steps and the joined parts of the paged and the cross attention.
 //
 // Allocations come from a memory pool owned by the library (one per device, created on first
 // use), not from the process's default pool, whose settings belong to the application.  The
