@@ -399,7 +399,9 @@ int sage_qk_norm_rope_append(const void* q, const void* k, const void* v, void* 
  * o_i = sum_j softmax_j(q_i . k_j * sm_scale) v_j over the keys the token sees: all kv_len[b] of them,
  * or, causal, keys j <= kv_len[b] - nq_b + i; query head h uses key head h / (Hq/Hk).  A token that
  * sees no key (kv_len < nq, or 0) gets 0.  Rows of o outside [cu_q[0], cu_q[B]) stay as they were.
- * Single tokens (nq_b = 1) and chunks of different lengths may be mixed in one call.
+ * Single tokens (nq_b = 1) and chunks of different lengths may be mixed in one call.  The kernel is chosen for the
+ * whole call, by the average number of new tokens: among many single tokens a long chunk that has many more keys than
+ * they is faster in a call of its own.
  * q, o: [T,Hq,d] (o may not overlap q), b strides unused; k_cache, v_cache: [num_pages][Hk][page_size][d];
  * page_table: [B][pages_per_seq]; cu_q: [B+1], ascending; kv_len: [B].  Hq is a multiple of Hk, at most
  * 128 times it.  Values of kv_len are taken into [0, pages_per_seq * page_size], of cu_q into [0, T];

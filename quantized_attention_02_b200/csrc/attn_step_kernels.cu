@@ -14,9 +14,9 @@
 //   - The products are taken transposed, with the keys on the tensor memory's 128 lanes and the 16 rows as
 //     the narrow side: S^T = K Q^T (N = 16) and O^T = V^T P^T (N = 32: the columns of hi, then of lo), so
 //     that a tile costs 16 short MMAs and a thread computes the few weights of one key.  With the rows on
-//     the lanes 112 of them would idle in the products and, worse, in the softmax: measured 125 us against
-//     100 us for a token of 32 heads over 131072 keys of 8 heads of 128 channels, both with the joining (86 us of it
-//     this kernel, 6.2 TB/s); 48 tokens over 5300 keys each on average take 165 us, 6.2 TB/s.
+//     the lanes 112 of them would idle in the products and, worse, in the softmax: measured 125 us in this
+//     kernel's frame against 97 us for a token of 32 heads over 131072 keys of 8 heads of 128 channels, both with the
+//     joining (86 us of it this kernel, 6.2 TB/s); 48 tokens over 5300 keys each on average take 163 us, 6.3 TB/s.
 //   - A row's offset is common to all lanes; it is taken from the first tile and moves only when a lane sees
 //     a score 8 above it (one vote per tile), so no tile but the first needs a maximum over lanes.
 //

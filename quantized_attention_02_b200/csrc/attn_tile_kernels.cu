@@ -3,9 +3,13 @@
 //
 // Mathematics as attn_pair_kernels.cu.  Bound: device memory at the lower end, the softmax at the upper: what
 // counts is that the key axis is read fast, so the CTA's two streams are one query tile with every other
-// key tile each, with a ring of their own, and the two (m, l, O) are joined at the end.  (As one stream of a
-// pair: 32 rows over 32768 keys of 8 heads 74 us instead of 43, 120 rows over 20 x 3000 keys 87 instead of 76.)
-// Few CTAs: the key axis is cut into parts, joined by attn_tile_join_kernel.
+// key tile each, with a ring of their own, and the two (m, l, O) are joined at the end.  As
+// pairs of tiles, with one stream in use (replays of a graph, cold L2): 32 rows over 32768 keys of 8 heads of 128 73 us
+// instead of 48, 100 rows over 4 x 1500 keys of 16 heads of 64 34 instead of 26, 120 rows over 20 x 3000 keys of 8 heads
+// of 128 87 instead of 84.
+// Few CTAs: the key axis is cut into parts, joined by attn_tile_join_kernel.  The last of these, 160 CTAs for 148
+// SMs, is not cut: its second round holds 12 CTAs (73 us in the profiler, 3.4 TB/s of keys and values; its bytes
+// alone would take 37).
 //
 // CTA: 12 warps, 512 TMEM columns, about 226 KB of shared memory.
 //   warp 0      TMA: Q once, then K and V tiles of 128 keys, K0 V0 K1 V1 ... in each stream's ring

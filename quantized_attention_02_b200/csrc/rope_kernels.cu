@@ -13,9 +13,12 @@
 // one tensor for its tokens (all eight loads first), so that what a lane needs besides -- weight and rotation,
 // multiplied together once -- is the same for all of them: y = r (x cw + x' sw), x' the pair's other channel
 // (its neighbour, or, half split, from another lane: shuffled as 16-bit pairs), r the row's norm.
-// 2 x (48 + 48) heads of 64 channels, 16384 tokens, fp16: 125 us, 6.4 TB/s (224 us with the norm, the weights and
-// both pair layouts worked out per head: 213 instructions per 16 bytes; 141 us with four heads and 256 threads,
-// 168 us with two heads).
+// 2 x (48 + 48) heads of 64 channels, 16384 tokens, fp16, interleaved: 123 us in the profiler, 6.56 TB/s; 128 us a call
+// (224 us with the norm, the weights and both pair layouts worked out per head: 213 instructions per 16 bytes; 141 us
+// with four heads and 256 threads, 168 us with two heads).
+// Half split pairs cost more: four shuffles per row and, at 64 registers (eight blocks per SM), 44 to 48 bytes of spills
+// a thread where the interleaved form has 8 at most.  8192 tokens of 32 + 8 + 8 heads of 128 into a cache: 37 us in the
+// profiler, 5.5 TB/s, with 67 % of the issue slots taken (62 % above).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

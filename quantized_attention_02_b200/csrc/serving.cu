@@ -139,8 +139,9 @@ int run_step(const sage::Attn16Launch& t, cudaStream_t st) {
 }
 
 // Pairs of query tiles: many items are dealt out whole, few have their key tiles cut into equal shares (of 512
-// keys at least).  16 sequences of up to 333 tokens over up to 4099 keys, 2.4 items per SM: 152 us cut, 177 us whole (the
-// last round is not full); 2 x 4096 tokens over 6001 keys, 6.9 per SM: 720 us cut (parts and joins), 643 us whole.
+// keys at least).  Replays of a graph, cold L2: 16 sequences of up to 333 tokens over up to 4099 keys, 2.4 items per SM,
+// 161 us cut, 180 whole (the last round is not full); a chunk of 2048 tokens over 16384 keys, 1.8 per SM, 434 cut, 455
+// whole; 2 x 4096 tokens over 6001 keys, 6.9 per SM, 663 cut (parts and joins), 635 whole.
 int run_pair(sage::Attn16Launch& l, cudaStream_t st) {
   sage::Attn16Args& a = l.a;
   const int sms = sm_count();
@@ -179,7 +180,14 @@ int run_tile(sage::Attn16Launch& l, int64_t ctas, cudaStream_t st) {
 constexpr int64_t kMaxKeys = 1 << 24;
 constexpr int kMaxSequences = 1 << 20;
 
-// Which kernel: by the rows (tokens x group) that a key head of an average sequence has.
+// Which kernel: by the rows (tokens x group) that a key head of an average sequence has.  Single tokens in the kernel for
+// few rows and in that for one tile, heads of 128, replays of a graph, cold L2: 48 of 32/8 heads over up to 8192 keys 180
+// and 203 us, one over 131072 keys 118 and 114, 16 of 16 heads of 64 over up to 1500 keys 34 and 38.
+// One choice for the call: a chunk among single tokens runs in the kernel that suits the average.  With 63 single tokens
+// over 4000 keys, 32/8 heads, and a chunk of 190 tokens (few rows) or 4096 (pairs) over as many keys, one call takes
+// 196 and 342 us, two calls 210 and 360.  Where the chunk has many more keys than the rest, two are better: 256 single tokens
+// over 200 keys and 700 tokens over 30000, 2150 us in one call (the kernel for few rows reads the keys once for every four
+// tokens), 365 in two.
 bool few_rows(int64_t tokens, int64_t sequences, int G) {
   return G <= sage::kStepRows && tokens * G <= sequences * sage::kStepRows;
 }
