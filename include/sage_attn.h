@@ -47,7 +47,7 @@ extern "C" {
 typedef enum {
   SAGE_OK = 0,
   SAGE_ERR_INVALID = -1,     /* null pointer, bad size, bad sm_scale, bad granularity */
-  SAGE_ERR_UNSUPPORTED = -2, /* valid request outside what the kernels implement (d, N) */
+  SAGE_ERR_UNSUPPORTED = -2, /* valid request outside what the kernels implement (d, N, page size, counts) */
   SAGE_ERR_CUDA = -3,        /* a CUDA runtime call or launch failed */
   SAGE_ERR_TIMEOUT = -4,     /* a kernel's bounded wait gave up (sage_last_device_error) */
   SAGE_ERR_NOMEM = -5,       /* workspace allocation failed */
@@ -353,6 +353,8 @@ int sage_attn_fwd_host_variant(const void* q, const void* k, const void* v, void
  *     aligned; every stride of a dimension larger than 1 is positive and a multiple of 8 elements.
  *     The attention calls take strides below 2^38 elements (a query's head stride: times Hq/Hk).
  *   - page_size is 16, 32, 64, 128 or 256 tokens; num_pages * page_size stays below 2^31.
+ *   - Scores and sums of weighted values overflow where fp32 does: the weights go up to 2^8, so that values of bf16
+ *     beyond 2^96 may come out infinite.
  *   - Index arrays (positions, slots, page_table, cu_q, kv_len, key_len) are int32 device memory,
  *     dense.  Their values are not known to the host: the kernels check them as stated and never
  *     access memory outside the tensors.

@@ -241,7 +241,8 @@ const char* sage_status_string(int status) {
   switch (status) {
     case SAGE_OK: return "ok";
     case SAGE_ERR_INVALID: return "invalid argument";
-    case SAGE_ERR_UNSUPPORTED: return "unsupported size (d must be 64 or 128; the INT32 debug entry also needs N a multiple of 128)";
+    case SAGE_ERR_UNSUPPORTED: return "unsupported size (d must be 64 or 128; the INT32 debug entry also needs N a multiple of 128; "
+                                      "paged caches: 16, 32, 64, 128 or 256 tokens a page; other limits stand with the entry in sage_attn.h)";
     case SAGE_ERR_CUDA: return "CUDA runtime error";
     case SAGE_ERR_TIMEOUT: return "a kernel wait timed out";
     case SAGE_ERR_NOMEM: return "workspace allocation failed";

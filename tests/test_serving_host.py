@@ -157,3 +157,7 @@ def test_attention_without_tokens_is_no_work(sa):
 
 def test_paged_attn_refuses_more_sequences_than_its_waits_allow(sa):
     assert paged(sa, B=(1 << 20) + 1) == UNSUPPORTED
+
+
+def test_the_unsupported_status_names_the_page_sizes(sa):
+    assert append(sa, page=48) == UNSUPPORTED and "page" in sa.sage_status_string(UNSUPPORTED)
